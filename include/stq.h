@@ -381,6 +381,98 @@ stq_status stq_import_slot(stq_pool *pool, int32_t req, int32_t slot, const void
  * (STQ_ERR_INDEX, STQ_ERR_NONFINITE or STQ_ERR_TIMEOUT; STQ_OK if clear). */
 stq_status stq_pool_check(stq_pool *pool, void *stream);
 
+/* ------------------------------------------------------------------ prompts and the 4-bit cache
+ *
+ * Types of token rows, and where they lie: element d (0..127) of head h of
+ * token t is at data + t * token_stride + h * head_stride + d, strides in
+ * elements (a part of a fused projection is such an array; strides may be 0
+ * or negative).  data and every row start on 16-byte boundaries.
+ */
+typedef enum { STQ_BF16 = 0, STQ_F16 = 1, STQ_F32 = 2 } stq_dtype;
+typedef struct {
+    const void *data;
+    int64_t token_stride, head_stride;
+} stq_rows;
+
+/*
+ * A cache of keys and values in 4 bits, for the softmax-attention layers of a
+ * stack whose linear-attention layers keep their states in a pool.  No
+ * counterpart in the paper; the codes are its symmetric absmax quantiser at
+ * b = 4 (Q(x) = s clip(round(x / s), -7, 7)), one binary16 scale for each group of
+ * 32 values of a head:
+ *     s = half(max |x| / 7),   z = clip(rint(x / s), -7, 7)   (s = 0: z = 0),
+ * IEEE fp32 division and round-half-to-even; the cache then stands for s z.
+ * Pages hold 64 tokens; token slot p * 64 + o is token o of page p.  The
+ * cache does not know which sequence a page belongs to: the caller keeps page
+ * tables and lengths.
+ *
+ * Layout of the 9216 bytes of one (page, key head); blocks are ordered
+ * [page][key head].  A 32-bit word holds eight codes in sign and magnitude:
+ * low codes j = 0..3 have their magnitude at bits [4j, 4j + 3) and their sign at
+ * bit 4j + 15, high codes at bits [4j + 16, 4j + 19) and (4j + 31) mod 32.
+ *   [0, 4096)     keys: token o at 64 o; the word at 16 t + 4 g of it holds
+ *                 dims 32 g + 8 t + j (low) and 32 g + 8 t + 4 + j (high)
+ *   [4096, 4608)  their scales: group g of token o at 8 o + 2 g
+ *   [4608, 8704)  values: pair p of tokens 2p (low codes) and 2p + 1 (high)
+ *                 at 128 p; the word at 16 ((i + 2p) mod 8) + 4 g of it holds
+ *                 dims 32 g + 4 i + j
+ *   [8704, 9216)  their scales: group g of token o at 16 (o / 2) + 4 g + 2 (o mod 2)
+ */
+#define STQ_CACHE_PAGE 64
+#define STQ_CACHE_BLOCK 9216
+typedef struct stq_cache stq_cache;
+
+/* Allocate a cache of num_pages pages of num_kv_heads heads (device memory,
+ * all codes zero) on the current device; head_dim must be 128. */
+stq_status stq_cache_create(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim, stq_cache **out);
+stq_status stq_cache_destroy(stq_cache *cache);
+stq_status stq_cache_bytes(const stq_cache *cache, size_t *bytes);
+
+/*
+ * Quantize n tokens' keys and values (all key heads) into the cache.
+ *   slot: device int64 [n], the token slot of each; a negative one is skipped
+ *         (a padded row), one beyond the cache is skipped and reported
+ *         (STQ_ERR_INDEX).  A slot named twice in a call has undefined content.
+ *   k, v: device rows of `dtype`, n tokens of num_kv_heads heads.
+ * A group that holds a NaN or an infinity, or whose scale overflows binary16,
+ * is stored as zeros and reported (STQ_ERR_NONFINITE), so that no other token
+ * is touched by it.  n == 0 is a no-op.
+ */
+stq_status stq_cache_append(stq_cache *cache, const int64_t *slot, int32_t n, int32_t dtype, const stq_rows *k,
+                            const stq_rows *v, void *stream);
+
+/* The values that the cache stands for: fp32 [n][num_kv_heads][128] (16-byte
+ * aligned) of keys and of values.  Rows of skipped slots are left as they were. */
+stq_status stq_cache_read(stq_cache *cache, const int64_t *slot, int32_t n, float *k_out, float *v_out, void *stream);
+
+/*
+ * Attention of one query token a sequence over the cache, grouped heads:
+ *   y[i][h] = sum_t softmax_t(scale q[i][h] . K_t) V_t over t < seq_len[i], with the
+ *   key head h / (num_heads / num_kv_heads).
+ *   page_table: device int32 [n][max_pages]; token t of sequence i is token
+ *               t % 64 of page page_table[i][t / 64].  Only entries that its
+ *               length reaches are read.  An entry outside the cache makes its 64
+ *               tokens invisible and is reported (STQ_ERR_INDEX).
+ *   seq_len:    device int32 [n], 0 <= seq_len[i] <= 64 max_pages (else the
+ *               sequence is skipped, its y left as it was, and STQ_ERR_INDEX
+ *               reported).  Length 0 gives y = 0.
+ *   q:          device rows of `dtype` (n tokens of num_heads heads); y: device
+ *               [n][num_heads][128] of the same type, 16-byte aligned.
+ *   workspace:  device scratch of at least stq_attn_decode_workspace bytes,
+ *               16-byte aligned, owned by the caller; its content need not be
+ *               kept between calls.  Calls that may overlap on the GPU (streams,
+ *               captured graphs) need one each.
+ * The same call gives the same bits: partial sums are joined in a fixed order.
+ * A head whose q is not finite (or not below 2^100) has an unspecified y.
+ */
+stq_status stq_attn_decode_workspace(const stq_cache *cache, int32_t n, int32_t num_heads, size_t *bytes);
+stq_status stq_attn_decode(stq_cache *cache, const int32_t *page_table, int32_t max_pages, const int32_t *seq_len,
+                           int32_t n, int32_t num_heads, int32_t dtype, const stq_rows *q, float scale, void *y,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* As stq_pool_check, for a cache's error word. */
+stq_status stq_cache_check(stq_cache *cache, void *stream);
+
 /* Number of kernel launches this library has issued in this process. */
 uint64_t stq_launch_count(void);
 

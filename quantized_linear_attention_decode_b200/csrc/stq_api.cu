@@ -12,9 +12,7 @@
 #include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "stq_internal.h"
+#include "stq_host.h"
 
 struct stq_pool {
     int kind = 0, R = 0, S = 0, H = 0;
@@ -46,6 +44,11 @@ struct stq_pool {
 
 namespace {
 
+using stq::cuda_fail;
+using stq::DeviceGuard;
+using stq::fault;
+using stq::NvtxRange;
+
 thread_local std::string g_last_error;
 std::atomic<uint64_t> g_launches{0};
 
@@ -58,18 +61,6 @@ stq_status fail(stq_status st, const char *fmt, ...)
     va_end(ap);
     g_last_error = buf;
     return st;
-}
-
-stq_status cuda_fail(cudaError_t e, const char *what)
-{
-    return fail(e == cudaErrorMemoryAllocation ? STQ_ERR_OOM : STQ_ERR_CUDA, "%s: %s", what,
-                cudaGetErrorString(e));
-}
-
-bool fault(const char *which)
-{
-    const char *f = std::getenv("STQ_FAULT");
-    return f != nullptr && std::strcmp(f, which) == 0;
 }
 
 // Layout of one head's page from its row bit widths and the bytes per row
@@ -202,34 +193,6 @@ stq::PoolView view(stq_pool *p)
     v.stall_tx = stall ? 16u : 0u;
     return v;
 }
-
-// An NVTX range over a launching call (a no-op unless a profiler is attached),
-// so that profiles attribute device work to the entry point that queued it.
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
-// Makes the pool's device current for the duration of a call.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            ok = false;
-            return;
-        }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 stq_status check_launch_args(const stq_pool *p, const int32_t *req, const int32_t *slot, int32_t n)
 {

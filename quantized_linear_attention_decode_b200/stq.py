@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(_PKG, "libstq.so")
 STQ_GDN, STQ_KDA = 0, 1
 STQ_SCALE_F16 = 1  # desc flag: per-row scales stored as IEEE binary16
 STQ_FIT_COLUMNS = 2  # desc flag: per-page column factors refitted at every quantisation
+STQ_BF16, STQ_F16, STQ_F32 = 0, 1, 2  # types of token rows
+STQ_CACHE_PAGE = 64  # tokens in a page of the 4-bit cache
 STQ_ALLOC_DP, STQ_ALLOC_LAGRANGE = 0, 1  # bit allocation methods
 STATUS = {0: "STQ_OK", 1: "STQ_ERR_ARG", 2: "STQ_ERR_OOM", 3: "STQ_ERR_CUDA", 4: "STQ_ERR_INDEX",
           5: "STQ_ERR_NONFINITE", 6: "STQ_ERR_UNSUPPORTED", 7: "STQ_ERR_TIMEOUT"}
@@ -30,7 +32,9 @@ EXPORTS = ("stq_pool_create", "stq_pool_destroy", "stq_pool_bytes", "stq_desc_by
            "stq_decode_step_static", "stq_decode_step_host", "stq_host_block_layout",
            "stq_decode_step_host_block", "stq_lifetime_weight", "stq_allocate_bits",
            "stq_export_slot", "stq_import_slot", "stq_pool_check", "stq_launch_count",
-           "stq_status_str", "stq_last_error")
+           "stq_status_str", "stq_last_error",
+           "stq_cache_create", "stq_cache_destroy", "stq_cache_bytes", "stq_cache_append", "stq_cache_read",
+           "stq_attn_decode_workspace", "stq_attn_decode", "stq_cache_check")
 
 
 class StqError(RuntimeError):
@@ -44,6 +48,10 @@ class _Desc(C.Structure):
                 ("num_heads", C.c_int32), ("d_k", C.c_int32), ("d_v", C.c_int32),
                 ("unit_bits", C.c_void_p), ("row_factor", C.c_void_p), ("col_factor", C.c_void_p),
                 ("flags", C.c_uint32), ("row_weight", C.c_void_p)]
+
+
+class _Rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 _lib = None
@@ -81,6 +89,14 @@ def load():
         "stq_export_slot": [P, I32, I32, P, SZ],
         "stq_import_slot": [P, I32, I32, P, SZ],
         "stq_pool_check": [P, P],
+        "stq_cache_create": [I32, I32, I32, P],
+        "stq_cache_destroy": [P],
+        "stq_cache_bytes": [P, P],
+        "stq_cache_append": [P, P, I32, I32, P, P, P],
+        "stq_cache_read": [P, P, I32, P, P, P],
+        "stq_attn_decode_workspace": [P, I32, I32, P],
+        "stq_attn_decode": [P, P, I32, P, I32, I32, I32, P, C.c_float, P, P, SZ, P],
+        "stq_cache_check": [P, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -398,3 +414,151 @@ def stq_status_str(status: int) -> str:
 
 def stq_last_error() -> str:
     return load().stq_last_error().decode()
+
+
+# ------------------------------------------------------------------ prompts and the 4-bit cache
+
+
+def _dtype(t, name="tensor"):
+    import torch
+    kinds = {torch.bfloat16: STQ_BF16, torch.float16: STQ_F16, torch.float32: STQ_F32}
+    if not isinstance(t, torch.Tensor) or t.dtype not in kinds:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
+    return kinds[t.dtype]
+
+
+def _rows(t, like, shape, name):
+    """A [tokens, heads, 128] tensor of any token and head strides as a stq_rows."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be on the CUDA device of the other tensors")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() > 0 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the 128 values of a head must be contiguous")
+    # a stride over one element is never taken
+    return _Rows(t.data_ptr(), t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0)
+
+
+def _on(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device} in one call")
+
+
+def _stream_of(stream, device):
+    import torch
+    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _scratch(workspace, nbytes, device, stream):
+    """The caller's workspace, or one from torch's allocator for the stream that the call runs on."""
+    import torch
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, nbytes
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+class Cache:
+    """Owner of one stq_cache handle (destroyed with the object)."""
+
+    def __init__(self, handle, num_pages, num_kv_heads, device):
+        self.handle = handle
+        self.num_pages, self.num_kv_heads, self.device = num_pages, num_kv_heads, device
+
+    def __del__(self):
+        self.close()
+
+    def close(self):
+        h = getattr(self, "handle", None)
+        self.handle = None
+        if h and _lib is not None:
+            try:
+                _lib.stq_cache_destroy(h)
+            except Exception:  # noqa: BLE001  (interpreter shutdown)
+                pass
+
+
+def stq_cache_create(num_pages: int, num_kv_heads: int, head_dim: int = 128) -> Cache:
+    import torch
+    h = C.c_void_p()
+    _check(load().stq_cache_create(int(num_pages), int(num_kv_heads), int(head_dim), C.byref(h)))
+    return Cache(h, int(num_pages), int(num_kv_heads), torch.device("cuda", torch.cuda.current_device()))
+
+
+def stq_cache_destroy(cache: Cache) -> None:
+    cache.close()
+
+
+def stq_cache_bytes(cache: Cache) -> int:
+    a = C.c_size_t()
+    _check(load().stq_cache_bytes(cache.handle, C.byref(a)))
+    return a.value
+
+
+def stq_cache_append(cache: Cache, slot, k, v, stream=None) -> None:
+    """Quantize the tokens k, v [n, num_kv_heads, 128] into the token slots slot (int64 [n], page * 64 + offset;
+    negative ones are skipped)."""
+    import torch
+    n = int(slot.numel())
+    shape = (n, cache.num_kv_heads, 128)
+    _on(cache.device, slot, k, v)
+    kr, vr = _rows(k, k, shape, "k"), _rows(v, k, shape, "v")
+    _check(load().stq_cache_append(cache.handle, _dev(slot, torch.int64, (n,), "slot"), n, _dtype(k, "k"), C.byref(kr),
+                                   C.byref(vr), _stream_of(stream, cache.device)))
+
+
+def stq_cache_read(cache: Cache, slot, k_out, v_out, stream=None) -> None:
+    """The fp32 values that the cache stands for at the token slots, into k_out and v_out [n, num_kv_heads, 128]."""
+    import torch
+    n = int(slot.numel())
+    shape = (n, cache.num_kv_heads, 128)
+    _on(cache.device, slot, k_out, v_out)
+    _check(load().stq_cache_read(cache.handle, _dev(slot, torch.int64, (n,), "slot"), n,
+                                 _dev(k_out, torch.float32, shape, "k_out"), _dev(v_out, torch.float32, shape, "v_out"),
+                                 _stream_of(stream, cache.device)))
+
+
+def stq_attn_decode_workspace(cache: Cache, n: int, num_heads: int) -> int:
+    """Bytes of scratch that stq_attn_decode needs."""
+    a = C.c_size_t()
+    _check(load().stq_attn_decode_workspace(cache.handle, int(n), int(num_heads), C.byref(a)))
+    return a.value
+
+
+def stq_attn_decode(cache: Cache, page_table, seq_len, q, y, scale=None, workspace=None, stream=None) -> None:
+    """Attention of one query token a sequence over the cache: page_table int32 [n, max_pages], seq_len int32 [n],
+    q and y [n, num_heads, 128]; scale defaults to 1 / sqrt(128)."""
+    import torch
+    n = int(seq_len.numel())
+    if page_table.dim() != 2 or q.dim() != 3:
+        raise ValueError("page_table must be [n, max_pages] and q [n, num_heads, 128]")
+    heads = int(q.shape[1])
+    shape = (n, heads, 128)
+    _on(cache.device, page_table, seq_len, q, y, workspace)
+    qr = _rows(q, q, shape, "q")
+    work, nbytes = _scratch(workspace, stq_attn_decode_workspace(cache, n, heads), cache.device, stream)
+    _check(load().stq_attn_decode(
+        cache.handle, _dev(page_table, torch.int32, (n, page_table.shape[1]), "page_table"), int(page_table.shape[1]),
+        _dev(seq_len, torch.int32, (n,), "seq_len"), n, heads, _dtype(q, "q"), C.byref(qr),
+        128 ** -0.5 if scale is None else float(scale), _dev(y, q.dtype, shape, "y"), C.c_void_p(work.data_ptr()), nbytes,
+        _stream_of(stream, cache.device)))
+
+
+def stq_cache_check(cache: Cache, stream=None, raise_on_error: bool = True) -> int:
+    st = load().stq_cache_check(cache.handle, _stream_of(stream, cache.device))
+    if raise_on_error:
+        _check(st)
+    return st
