@@ -407,23 +407,26 @@ typedef struct {
  * tables and lengths.
  *
  * Layout of the 9216 bytes of one (page, key head); blocks are ordered
- * [page][key head].  A 32-bit word holds eight codes in sign and magnitude:
- * low codes j = 0..3 have their magnitude at bits [4j, 4j + 3) and their sign at
- * bit 4j + 15, high codes at bits [4j + 16, 4j + 19) and (4j + 31) mod 32.
- *   [0, 4096)     keys: token o at 64 o; the word at 16 t + 4 g of it holds
+ * [page][key head].  A code is stored as z + 8; a 32-bit word holds eight: code j
+ * of the low half (j = 0..3) at bits [4j, 4j + 4), of the high half at bits
+ * [4j + 16, 4j + 20).
+ * A block has two halves of 4608 bytes, tokens 0..31 and 32..63 of the page; in
+ * a half, with its token o = 0..31:
+ *   [0, 2048)     keys: token o at 64 o; the word at 16 t + 4 g of it holds
  *                 dims 32 g + 8 t + j (low) and 32 g + 8 t + 4 + j (high)
- *   [4096, 4608)  their scales: group g of token o at 8 o + 2 g
- *   [4608, 8704)  values: pair p of tokens 2p (low codes) and 2p + 1 (high)
+ *   [2048, 2304)  their scales: group g of token o at 8 o + 2 g
+ *   [2304, 4352)  values: pair p of tokens 2p (low halves) and 2p + 1 (high)
  *                 at 128 p; the word at 16 ((i + 2p) mod 8) + 4 g of it holds
  *                 dims 32 g + 4 i + j
- *   [8704, 9216)  their scales: group g of token o at 16 (o / 2) + 4 g + 2 (o mod 2)
+ *   [4352, 4608)  their scales: group g of token o at 16 (o / 2) + 4 g + 2 (o mod 2)
+ * A new cache's scales are zero, so that it stands for zeros.
  */
 #define STQ_CACHE_PAGE 64
 #define STQ_CACHE_BLOCK 9216
 typedef struct stq_cache stq_cache;
 
 /* Allocate a cache of num_pages pages of num_kv_heads heads (device memory,
- * all codes zero) on the current device; head_dim must be 128. */
+ * standing for zeros) on the current device; head_dim must be 128. */
 stq_status stq_cache_create(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim, stq_cache **out);
 stq_status stq_cache_destroy(stq_cache *cache);
 stq_status stq_cache_bytes(const stq_cache *cache, size_t *bytes);

@@ -1,15 +1,19 @@
 // stq_cache.cu -- keys and values held in 4 bits, and attention of single tokens over them (sm_100a).
 //
-// A page of 64 tokens of one key head is one 9216-byte block: 64 bytes of codes
-// and four binary16 scales for each token's key, and the same for its value
-// (layout: include/stq.h).  The block is laid out for the reader: one bulk copy
-// brings it into shared memory, and one 16-byte read gives a thread exactly the
-// codes that its matrix fragments need.
+// A page of 64 tokens of one key head is one 9216-byte block of two halves of 32
+// tokens: 64 bytes of codes and four binary16 scales for each token's key, and the
+// same for its value (layout: include/stq.h).  A half is laid out for the reader: one
+// bulk copy brings it into shared memory, and one 16-byte read gives a thread exactly
+// the codes that its matrix fragments need.
 //
-// Codes are kept in sign and magnitude.  A word rotated right by 4 j and masked
-// with 0x80078007 is a pair of binary16 subnormals, z 2^-24 each: the tensor core
-// takes them as they are, so a pair of codes costs two integer instructions and
-// no conversion, and the 2^24 goes into a factor that is applied anyway.
+// A code z is kept as u = z + 8 in four bits.  (w & 0x000f000f) | 0x64006400 is a pair of
+// binary16 values 1024 + u, and with 0x00f000f0 one of 1024 + 16 u; a packed subtraction
+// makes z and 16 z of them, exactly, and the 16 goes into the other operand.  Eight codes
+// cost a shift, four logic operations and four packed additions.  (Taken without the
+// subtraction, as binary16 subnormals u 2^-24 with the offset removed from the sums, the
+// arithmetic was 12 % fewer instructions and no faster, and the sums lost up to 10 bits: the
+// tensor core lines products up by their operands' nominal exponents.)
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -26,11 +30,9 @@ namespace stq {
 namespace {
 
 constexpr int kPage = STQ_CACHE_PAGE, kBlock = STQ_CACHE_BLOCK;
-constexpr int kKeyScales = 4096, kValues = 4608, kValueScales = 8704;  // offsets inside a block
-constexpr uint32_t kCodes = 0x80078007u;  // sign and magnitude of one low and one high code
-constexpr uint32_t kLow = 0x0888F777u;    // bits of the four low codes of a word
-
-static_assert(kValueScales + 512 == kBlock && kD == 128, "block layout");
+constexpr int kHalf = kPage / 2, kHalfBlock = kBlock / 2;              // tokens and bytes of a half
+constexpr int kKeyScales = 2048, kValues = 2304, kValueScales = 4352;  // offsets inside it
+static_assert(kValueScales + 8 * kHalf == kHalfBlock && kD == 128, "block layout");
 
 struct CacheView {
     uint8_t *data;
@@ -50,27 +52,16 @@ struct Rows {
 // 8 dims a lane, so that a group of 32 values is four lanes.  Bound by memory
 // (the rows in, 144 bytes out); not tuned further.
 
-// The word of eight codes z[0..3] (low) and z[4..7] (high).
-__device__ __forceinline__ uint32_t low_codes(const int (&z)[4])
+// The 16 bits of four codes, and back.
+__device__ __forceinline__ uint32_t pack4(const int *z)
 {
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t m = static_cast<uint32_t>(abs(z[j]));
-        w |= m << (4 * j) | (z[j] < 0 ? 1u : 0u) << (4 * j + 15);
-    }
-    return w;
+    return static_cast<uint32_t>(z[0] + 8 | (z[1] + 8) << 4 | (z[2] + 8) << 8 | (z[3] + 8) << 12);
 }
 
-__device__ __forceinline__ void word_codes(uint32_t w, float (&z)[8])
+__device__ __forceinline__ void unpack4(uint32_t w, float *z)
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t p = __funnelshift_r(w, w, 4 * j) & kCodes;
-        const float lo = static_cast<float>(p & 7u), hi = static_cast<float>(p >> 16 & 7u);
-        z[j] = p & 0x8000u ? -lo : lo;
-        z[4 + j] = p & 0x80000000u ? -hi : hi;
-    }
+    for (int j = 0; j < 4; ++j) z[j] = static_cast<float>(static_cast<int>(w >> (4 * j) & 15u) - 8);
 }
 
 __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long long *slot, int n, int dtype, Rows k, Rows v)
@@ -106,34 +97,23 @@ __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long lon
         sf = 0.0f;
         if ((lane & 3) == 0) atomicOr(c.err, kErrNonFinite);
     }
-    int lo[4], hi[4];
+    int z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        float z = sf > 0.0f ? rintf(__fdiv_rn(x[j], sf)) : 0.0f;
-        z = fminf(fmaxf(z, -7.0f), 7.0f);
-        (j < 4 ? lo : hi)[j & 3] = static_cast<int>(z);
+        const float y = sf > 0.0f ? rintf(__fdiv_rn(x[j], sf)) : 0.0f;
+        z[j] = static_cast<int>(fminf(fmaxf(y, -7.0f), 7.0f));
     }
-    const int o = static_cast<int>(at & (kPage - 1)), g = l >> 2, t = l & 3;
-    uint8_t *b = c.block(static_cast<int>(at / kPage), h);
+    const int o = static_cast<int>(at & (kHalf - 1)), g = l >> 2, t = l & 3;
+    uint8_t *b = c.block(static_cast<int>(at / kPage), h) + (at & kHalf ? kHalfBlock : 0);
     if (key) {
-        const uint32_t w0 = low_codes(lo), w1 = low_codes(hi);
-        *reinterpret_cast<uint32_t *>(b + 64 * o + 16 * t + 4 * g) = w0 | __funnelshift_l(w1, w1, 16);
+        *reinterpret_cast<uint32_t *>(b + 64 * o + 16 * t + 4 * g) = pack4(z) | pack4(z + 4) << 16;
         if (t == 0) *reinterpret_cast<__half *>(b + kKeyScales + 8 * o + 2 * g) = s;
     } else {
-        // a value word holds two tokens: each append changes its own token's bits
-        // only, with an AND and an OR, so tokens of one pair may come in one call
         const int p = o >> 1;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t w = half ? low_codes(hi) : low_codes(lo), others = ~kLow;
-            if (o & 1) {
-                w = __funnelshift_l(w, w, 16);
-                others = kLow;
-            }
-            uint32_t *to = reinterpret_cast<uint32_t *>(b + kValues + 128 * p + 16 * ((2 * t + half + 2 * p) & 7) + 4 * g);
-            atomicAnd(to, w | others);
-            atomicOr(to, w);
-        }
+        for (int half = 0; half < 2; ++half)
+            *reinterpret_cast<uint16_t *>(b + kValues + 128 * p + 16 * ((2 * t + half + 2 * p) & 7) + 4 * g + 2 * (o & 1)) =
+                static_cast<uint16_t>(pack4(z + 4 * half));
         if (t == 0) *reinterpret_cast<__half *>(b + kValueScales + 16 * p + 4 * g + 2 * (o & 1)) = s;
     }
 }
@@ -151,22 +131,18 @@ __global__ void __launch_bounds__(256) read_kernel(CacheView c, const long long 
         if (lane == 0) atomicOr(c.err, kErrIndex);
         return;
     }
-    const int o = static_cast<int>(at & (kPage - 1)), g = l >> 2, t = l & 3, p = o >> 1;
-    const uint8_t *b = c.block(static_cast<int>(at / kPage), h);
+    const int o = static_cast<int>(at & (kHalf - 1)), g = l >> 2, t = l & 3, p = o >> 1;
+    const uint8_t *b = c.block(static_cast<int>(at / kPage), h) + (at & kHalf ? kHalfBlock : 0);
     float z[8], s;
     if (key) {
-        word_codes(*reinterpret_cast<const uint32_t *>(b + 64 * o + 16 * t + 4 * g), z);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(b + 64 * o + 16 * t + 4 * g);
+        unpack4(w, z);
+        unpack4(w >> 16, z + 4);
         s = __half2float(*reinterpret_cast<const __half *>(b + kKeyScales + 8 * o + 2 * g));
     } else {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t w = *reinterpret_cast<const uint32_t *>(b + kValues + 128 * p + 16 * ((2 * t + half + 2 * p) & 7) + 4 * g);
-            if (o & 1) w = __funnelshift_l(w, w, 16);
-            float y[8];
-            word_codes(w, y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[4 * half + j] = y[j];
-        }
+        for (int half = 0; half < 2; ++half)
+            unpack4(*reinterpret_cast<const uint16_t *>(b + kValues + 128 * p + 16 * ((2 * t + half + 2 * p) & 7) + 4 * g + 2 * (o & 1)), z + 4 * half);
         s = __half2float(*reinterpret_cast<const __half *>(b + kValueScales + 16 * p + 4 * g + 2 * (o & 1)));
     }
     float4 *to = reinterpret_cast<float4 *>((key ? k : v) + static_cast<size_t>(item) * kD + 8 * l);
@@ -178,15 +154,17 @@ __global__ void __launch_bounds__(256) read_kernel(CacheView c, const long long 
 //
 // Bound by reading the cache: 144 bytes a token and key head, 256 codes of it to
 // unpack.  The units of work are (sequence, key head and block of query heads,
-// page) in that order; every CTA takes an equal contiguous share of all units, so
+// half page) in that order; every warp takes an equal contiguous share of all units, so
 // a few long sequences and many ragged ones fill the machine alike.  A share
-// falls into segments, the runs of pages of one (sequence, head block).  The
-// segments that a CTA does not finish alone leave an unnormalised partial sum,
-// and join_kernel adds those in the order of the CTAs.
+// falls into segments, the runs of units of one (sequence, head block).  The
+// segments that a warp does not finish alone leave an unnormalised partial sum,
+// and join_kernel adds those in the order of the warps.  (Shares a CTA at a time,
+// its warps joined at the end of every segment, took 218 us on 64 ragged sequences
+// up to 8192 tokens: the joins of short segments stand in a row.)  Where there are
+// fewer halves than half of the warps, a unit is a quarter of a page.
 //
-// Within a CTA each warp takes every kWarps-th page of the segment with its own
-// two-stage ring, softmax statistics and accumulators, and the warps are joined at
-// the segment's end.  Per page and block of eight heads, with mma.sync (the
+// A warp has its own ring of halves in shared memory, filled by bulk copies that run
+// ahead over the segments.  Per half and block of eight heads, with mma.sync (the
 // matrices have 8 columns, far below a tcgen05 tile's 128 rows):
 //   S = K q^T      16 tokens x 8 heads a tile.  A group of 32 dims is two steps of
 //                  16, so its binary16 scale multiplies the fp32 sums, 4 products
@@ -194,19 +172,24 @@ __global__ void __launch_bounds__(256) read_kernel(CacheView c, const long long 
 //   O^T += V^T P^T 16 dims x 8 heads a tile; a value's scale goes into P.  P is
 //                  rounded to binary16, and so is its product with the scale: 2^-11 of a
 //                  weight each, below the output's own rounding in bf16.
-// P is 2^15 exp2(x - R) with R at least the running maximum of x + max(0, log2 of the
-// page's largest value scale), so that P times a scale stays below 2^15 while small
-// weights keep their bits: what falls below binary16's subnormals is 2^-39 of the
+// P is 2^11 exp2(x - R) with R at least the running maximum, less 4, of x + max(0, log2 of the
+// unit's largest value scale), so that P times a scale stays below 2^15 while small
+// weights keep their bits: what falls below binary16's subnormals is 2^-36 of the
 // largest weight.  Sums are fp32.
 
-constexpr int kWarps = 4;
-constexpr int kStagesW = 2;
+constexpr int kWarps = 4;   // of a CTA; they share nothing but its memory
+constexpr int kUnit = 2;     // halves of a unit
+constexpr int kStagesW = 2;  // units in a warp's ring
+constexpr int kUnitTokens = kUnit * kHalf, kUnitBytes = kUnit * kHalfBlock;
+
+constexpr float kSlack = 4.0f;           // how far a score may lie above R
 
 struct AttnArgs {
     CacheView c;
     const int32_t *table;
     const int32_t *seq_len;
     int max_pages, n, heads, group, blocks;  // blocks: of 8 NT query heads, for each key head
+    int warps;                               // of the launch
     int dtype;
     Rows q;
     float scale_log2;  // scale log2(e)
@@ -234,21 +217,48 @@ __device__ __forceinline__ long long pages_before(const AttnArgs &a, int upto)
     return sum;
 }
 
-// Where a walk over the units stands: page `page` of sequence seq, head block sub.
+// How all units are shared out: `warps` shares (no more than there are units) of q or q + 1 units,
+// the longer ones first.
+struct Shares {
+    int subs, shift;  // segments of a sequence; 2^shift units of a page (1 or 4)
+    long long units, q;
+    int warps, longer;
+    __device__ long long begin(int w) const { return q * w + min(w, longer); }
+    __device__ int owner(long long u) const
+    {
+        const long long past = u - (q + 1) * longer;
+        return static_cast<int>(past < 0 ? u / (q + 1) : longer + past / q);
+    }
+};
+
+__device__ __forceinline__ Shares shares_of(const AttnArgs &a)
+{
+    Shares s;
+    s.subs = a.c.heads * a.blocks;
+    s.units = pages_before(a, a.n) * s.subs;
+    s.shift = s.units * 4 <= a.warps ? 2 : kUnit == 1 ? 1 : 0;
+    s.units <<= s.shift;
+    s.warps = static_cast<int>(min(static_cast<long long>(a.warps), max(s.units, 1ll)));
+    s.q = s.units / s.warps;
+    s.longer = static_cast<int>(s.units - s.q * s.warps);
+    return s;
+}
+
+// Where a walk over the units stands: unit `unit` of the `units` of sequence seq, segment sub.
 struct Walk {
-    int seq, pages, sub, page;
+    int seq, sub, unit, units;
 };
 
 // The place of unit u of all (u below their number); the whole warp calls it.
-__device__ __forceinline__ Walk place_of(const AttnArgs &a, long long u, int subs)
+__device__ __forceinline__ Walk place_of(const AttnArgs &a, const Shares &s, long long u)
 {
     const int lane = threadIdx.x & 31;
-    Walk w{0, 0, 0, 0};
+    Walk w{0, 0, 0, 1};
     long long base = 0;
     for (int first = 0; first < a.n; first += 32) {
         const int i = first + lane;
-        const int p = i < a.n ? pages_of(a, i) : 0;
-        long long upto = static_cast<long long>(p) * subs;
+        const int mine = i < a.n ? pages_of(a, i) << s.shift : 0;
+        long long upto = static_cast<long long>(mine) * s.subs;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, upto, d);
@@ -257,12 +267,11 @@ __device__ __forceinline__ Walk place_of(const AttnArgs &a, long long u, int sub
         const uint32_t past = __ballot_sync(0xffffffffu, base + upto > u);
         if (past) {
             const int who = __ffs(past) - 1;
-            const long long end = __shfl_sync(0xffffffffu, base + upto, who);
             w.seq = first + who;
-            w.pages = __shfl_sync(0xffffffffu, p, who);
-            const long long in = u - (end - static_cast<long long>(w.pages) * subs);
-            w.sub = static_cast<int>(in / w.pages);
-            w.page = static_cast<int>(in - static_cast<long long>(w.sub) * w.pages);
+            w.units = __shfl_sync(0xffffffffu, mine, who);
+            const long long in = u - (base + __shfl_sync(0xffffffffu, upto, who) - static_cast<long long>(w.units) * s.subs);
+            w.sub = static_cast<int>(in / w.units);
+            w.unit = static_cast<int>(in - static_cast<long long>(w.sub) * w.units);
             return w;
         }
         base += __shfl_sync(0xffffffffu, upto, 31);
@@ -270,445 +279,489 @@ __device__ __forceinline__ Walk place_of(const AttnArgs &a, long long u, int sub
     return w;
 }
 
-// The next head block, or the next sequence that has pages.
-__device__ __forceinline__ void next_segment(const AttnArgs &a, Walk &w, int subs)
+// The next segment, of this sequence or of the next one that has pages.
+__device__ __forceinline__ void next_segment(const AttnArgs &a, const Shares &s, Walk &w)
 {
-    w.page = 0;
-    if (++w.sub < subs) return;
+    w.unit = 0;
+    if (++w.sub < s.subs) return;
     w.sub = 0;
     do {
         ++w.seq;
-        w.pages = w.seq < a.n ? pages_of(a, w.seq) : 0;
-    } while (w.seq < a.n && w.pages == 0);
+        w.units = w.seq < a.n ? pages_of(a, w.seq) << s.shift : 0;
+    } while (w.seq < a.n && w.units == 0);
 }
 
-// A warp's pages in the order it takes them, running ahead of the arithmetic: the
-// page numbers of 32 pages at a time are held one in each lane.
+// A share's units in their order, running ahead of the arithmetic: the page numbers
+// of 32 units at a time are held one in each lane.
 struct Feed {
     Walk w;
-    long long left;  // units from the segment's first page in the share to the share's end
-    int page, end;   // this warp's next page in the segment, and the segment's end in the share
-    int ids, first;  // ids: lane j has the page number of page first + j * kWarps
+    int left;        // units of the share that are still to come
+    int first, end;  // lane j has the page number of unit first + j of the segment, up to `end`
+    int ids;
 };
 
-__device__ __forceinline__ void feed_segment(const AttnArgs &a, Feed &f, int warp)
+// The page number of the next unit (-1: none left; -2: outside the cache) its key head and the half.
+__device__ __forceinline__ int feed_next(const AttnArgs &a, const Shares &s, Feed &f, int *head, int *half)
 {
-    const long long room = f.w.page + f.left;
-    f.end = room < f.w.pages ? static_cast<int>(room) : f.w.pages;
-    f.page = f.w.page + warp;
-    f.first = f.page - 32 * kWarps;
-}
-
-// The page number of the warp's next page (-1: none left; -2: outside the cache).
-__device__ __forceinline__ int feed_next(const AttnArgs &a, Feed &f, int warp, int subs, int *head)
-{
-    while (f.page >= f.end) {
-        f.left -= f.end - f.w.page;
-        if (f.left <= 0) return -1;
-        next_segment(a, f.w, subs);
-        feed_segment(a, f, warp);
+    if (f.left == 0) return -1;
+    if (f.w.unit == f.w.units) {
+        next_segment(a, s, f.w);
+        f.end = 0;
     }
-    if (f.page >= f.first + 32 * kWarps) {
-        f.first = f.page;
-        const int p = f.first + (threadIdx.x & 31) * kWarps;
-        f.ids = p < f.end ? a.table[static_cast<size_t>(f.w.seq) * a.max_pages + p] : 0;
+    if (f.w.unit >= f.end) {
+        f.first = f.w.unit;
+        f.end = min(f.first + 32, f.w.units);
+        const int u = f.first + static_cast<int>(threadIdx.x & 31);
+        f.ids = u < f.end ? a.table[static_cast<size_t>(f.w.seq) * a.max_pages + (u >> s.shift)] : 0;
     }
-    const int id = __shfl_sync(0xffffffffu, f.ids, (f.page - f.first) / kWarps);
-    f.page += kWarps;
+    const int id = __shfl_sync(0xffffffffu, f.ids, f.w.unit - f.first);
     *head = f.w.sub / a.blocks;
+    *half = s.shift == 2 ? f.w.unit >> 1 & 1 : kUnit == 1 ? f.w.unit & 1 : 0;
+    ++f.w.unit;
+    --f.left;
     return id < 0 || id >= a.c.pages ? -2 : id;
 }
 
-template <int NT>
 struct __align__(128) AttnSmem {
-    uint8_t stage[kWarps][kStagesW][kBlock];
-    float sum[8 * NT][kD + 4];
-    float top[kWarps][8 * NT], weight[kWarps][8 * NT];
+    uint8_t stage[kWarps][kStagesW][kUnitBytes];
     unsigned long long full[kWarps][kStagesW];
 };
 
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int j) { return __funnelshift_r(w, w, 4 * j) & kCodes; }
+__device__ __forceinline__ float2 floats_of(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+
+// The running state of one segment: lane (g, t) has columns 2t, 2t + 1 of each block of eight heads.
+template <int NT>
+struct Segment {
+    uint32_t qf[NT][4][4];  // q as B fragments
+    float fac[NT][2];       // from products of codes to scores in units of log 2
+    float o[8][NT][4], top[NT][2], weight[NT][2];
+};
+
+// q: step (group gi, j) takes dims 32 gi + 8 t + j and + 4 + j of head g, scaled by a power of two
+// so that every row lies high in binary16's range (the largest value in [2^13, 2^14): a 16-bit q is
+// exact down to 2^-20 of it), and by 1 / 16 where the codes come as 16 u.
+template <int NT>
+__device__ __forceinline__ void begin_segment(const AttnArgs &a, Segment<NT> &sg, int seq, int h0, int nh)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float x[4][8], big = 0.0f;
+        const int h = nt * 8 + g;
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+            if (h < nh) load8(a.q.data, seq * a.q.token_stride + (h0 + h) * a.q.head_stride + 32 * gi + 8 * t, a.dtype, x[gi]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (h >= nh) x[gi][j] = 0.0f;
+                big = fmaxf(big, fabsf(x[gi][j]));
+            }
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^e <= big < 2^(e + 1), within what both 2^e and 2^-e can be; the scale's sign goes into q, so that
+        // the largest product gives the largest score
+        const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 100);
+        const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23), a.scale_log2);
+        const float f = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float fold = j & 1 ? 0.0625f * down : down;
+                const __half2 v = __floats2half2_rn(x[gi][j] * fold, x[gi][4 + j] * fold);
+                sg.qf[nt][gi][j] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+        sg.fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+        sg.fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        sg.top[nt][0] = sg.top[nt][1] = -INFINITY;
+        sg.weight[nt][0] = sg.weight[nt][1] = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) sg.o[m][nt][0] = sg.o[m][nt][1] = sg.o[m][nt][2] = sg.o[m][nt][3] = 0.0f;
+    }
+}
+
+// (a & b) | c in one instruction (two constants, which the compiler would take in two steps).
+__device__ __forceinline__ uint32_t select_or(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// Four pairs of codes of a word as binary16: z, 16 z, z, 16 z.  u in the mantissa of 2^10, or 16 u,
+// less what the offset makes of it: exact.
+__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t (&p)[4])
+{
+    const uint32_t v = w >> 8;
+    p[0] = select_or(w, 0x000f000fu, 0x64006400u);
+    p[1] = select_or(w, 0x00f000f0u, 0x64006400u);
+    p[2] = select_or(v, 0x000f000fu, 0x64006400u);
+    p[3] = select_or(v, 0x00f000f0u, 0x64006400u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 z = __hadd2(*reinterpret_cast<const __half2 *>(&p[j]), __float2half2_rn(j & 1 ? -1152.0f : -1032.0f));
+        p[j] = *reinterpret_cast<const uint32_t *>(&z);
+    }
+}
+
+// MT tiles of 16 tokens in shared memory, from tile m0 on; `valid` of the tokens there are the
+// sequence's, at least one of them in these tiles.
+template <int NT, int MT>
+__device__ __forceinline__ void take_unit(Segment<NT> &sg, const uint8_t *b, int valid, int m0)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float x[MT][NT][4];  // scores in units of fac
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const uint8_t *bh = b + (mt >> 1) * kHalfBlock;
+        const int r0 = (m0 + (mt & 1)) * 16 + g, r1 = r0 + 8;
+        const uint4 ka = *reinterpret_cast<const uint4 *>(bh + 64 * r0 + 16 * t);
+        const uint4 kb = *reinterpret_cast<const uint4 *>(bh + 64 * r1 + 16 * t);
+        const uint2 sa = *reinterpret_cast<const uint2 *>(bh + kKeyScales + 8 * r0);
+        const uint2 sb = *reinterpret_cast<const uint2 *>(bh + kKeyScales + 8 * r1);
+        const float2 sa0 = floats_of(sa.x), sa1 = floats_of(sa.y), sb0 = floats_of(sb.x), sb1 = floats_of(sb.y);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        const float fa[4] = {sa0.x, sa0.y, sa1.x, sa1.y}, fb[4] = {sb0.x, sb0.y, sb1.x, sb1.y};
+        float c[4][NT][4];
+        uint32_t pa[4][4], pb[4][4];
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+            pairs_of(wa[gi], pa[gi]);
+            pairs_of(wb[gi], pb[gi]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_f16_from(c[gi][nt], 0.0f, 0.0f, 0.0f, 0.0f, pa[gi][0], pb[gi][0], pa[gi][1], pb[gi][1], sg.qf[nt][gi][0], sg.qf[nt][gi][1]);
+            }
+        }
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(c[gi][nt], pa[gi][2], pb[gi][2], pa[gi][3], pb[gi][3], sg.qf[nt][gi][2], sg.qf[nt][gi][3]);
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float f = j < 2 ? fa[gi] : fb[gi];
+                    x[mt][nt][j] = gi == 0 ? f * c[gi][nt][j] : fmaf(f, c[gi][nt][j], x[mt][nt][j]);
+                }
+    }
+    if (valid < MT * 16 + m0 * 16) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if ((m0 + mt) * 16 + g + (j >> 1) * 8 >= valid) x[mt][nt][j] = -INFINITY;
+    }
+    // the largest value scale (positive binary16 values order as integers), as a power of two >= 1
+    uint32_t mu = 0;
+#pragma unroll
+    for (int half = 0; half < (MT + 1) / 2; ++half) {
+        const uint2 vs = *reinterpret_cast<const uint2 *>(b + half * kHalfBlock + kValueScales + 8 * lane);
+        mu = __vmaxu2(mu, __vmaxu2(vs.x, vs.y));
+    }
+    const uint32_t biggest = __reduce_max_sync(0xffffffffu, max(mu & 0xffffu, mu >> 16));
+    const float up = static_cast<float>(max(0, static_cast<int>(biggest >> 10) - 14));
+    // R moves only when a score is 2^4 above it, so that the lanes seldom have to agree on a new one
+    bool moves = false;
+    float m[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float y = fmaxf(x[0][nt][j], x[0][nt][2 + j]);
+#pragma unroll
+            for (int mt = 1; mt < MT; ++mt) y = fmaxf(y, fmaxf(x[mt][nt][j], x[mt][nt][2 + j]));
+            m[nt][j] = fmaf(y, sg.fac[nt][j], up);
+            moves |= m[nt][j] > sg.top[nt][j] + kSlack;
+        }
+    if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float y = m[nt][j];
+                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                y = fmaxf(y, sg.top[nt][j]);
+                f[j] = exp2_approx(sg.top[nt][j] - y);
+                sg.top[nt][j] = y;
+                sg.weight[nt][j] *= f[j];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sg.o[k][nt][0] *= f[0];
+                sg.o[k][nt][1] *= f[1];
+                sg.o[k][nt][2] *= f[0];
+                sg.o[k][nt][3] *= f[1];
+            }
+        }
+    }
+    float base[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) base[nt][j] = 15.0f - kSlack - sg.top[nt][j];
+    const int pos = ((g + 2 * t) & 7) * 16;  // a tile's pairs t and t + 4 lie rotated by 2 t
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const uint8_t *bh = b + (mt >> 1) * kHalfBlock;
+        const int pr = (m0 + (mt & 1)) * 8 + t;
+        const uint4 va = *reinterpret_cast<const uint4 *>(bh + kValues + 128 * pr + pos);
+        const uint4 vb = *reinterpret_cast<const uint4 *>(bh + kValues + 128 * (pr + 4) + pos);
+        const uint4 ua = *reinterpret_cast<const uint4 *>(bh + kValueScales + 16 * pr);
+        const uint4 ub = *reinterpret_cast<const uint4 *>(bh + kValueScales + 16 * (pr + 4));
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+        const uint32_t fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w};
+        __half2 b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] = exp2_approx(fmaf(x[mt][nt][j], sg.fac[nt][j & 1], base[nt][j & 1]));
+            sg.weight[nt][0] += e[0] + e[2];
+            sg.weight[nt][1] += e[1] + e[3];
+            const __half2 c0 = __floats2half2_rn(e[0], e[1]), c1 = __floats2half2_rn(e[2], e[3]);
+            const uint32_t d0 = transpose8(*reinterpret_cast<const uint32_t *>(&c0));
+            const uint32_t d1 = transpose8(*reinterpret_cast<const uint32_t *>(&c1));
+            b0[nt] = *reinterpret_cast<const __half2 *>(&d0);
+            b1[nt] = *reinterpret_cast<const __half2 *>(&d1);
+        }
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+            uint32_t pa[4], pb[4];
+            pairs_of(wa[gi], pa);
+            pairs_of(wb[gi], pb);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const __half2 e0 = __hmul2(b0[nt], *reinterpret_cast<const __half2 *>(&fa[gi]));
+                const __half2 e1 = __hmul2(b1[nt], *reinterpret_cast<const __half2 *>(&fb[gi]));
+                const uint32_t u0 = *reinterpret_cast<const uint32_t *>(&e0), u1 = *reinterpret_cast<const uint32_t *>(&e1);
+                mma_f16(sg.o[2 * gi][nt], pa[0], pa[1], pb[0], pb[1], u0, u1);
+                mma_f16(sg.o[2 * gi + 1][nt], pa[2], pa[3], pb[2], pb[3], u0, u1);
+            }
+        }
+    }
+}
+
+// Four consecutive values of a row of y, rounded once.
+__device__ __forceinline__ void store4(void *y, int64_t at, int dtype, const float (&v)[4])
+{
+    if (dtype == STQ_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        return;
+    }
+    uint2 w;
+    if (dtype == STQ_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+        const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+        w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + at) = w;
+}
+
+// The segment's result: y itself where the warp had all of it (part == nullptr), else a partial.
+template <int NT>
+__device__ __forceinline__ void end_segment(const AttnArgs &a, Segment<NT> &sg, int seq, int h0, int nh, float *part)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float l = sg.weight[nt][j];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int h = nt * 8 + 2 * t + j;
+            if (h >= nh) continue;
+            const float f = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no weight at all: every page absent
+#pragma unroll
+            for (int gi = 0; gi < 4; ++gi) {
+                // rows 8 to 15 of a tile are sums of 16 z
+                const float v[4] = {sg.o[2 * gi][nt][j] * f, sg.o[2 * gi][nt][2 + j] * (0.0625f * f),
+                                    sg.o[2 * gi + 1][nt][j] * f, sg.o[2 * gi + 1][nt][2 + j] * (0.0625f * f)};
+                if (part) *reinterpret_cast<float4 *>(part + h * kD + 32 * gi + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
+                else store4(a.y, (static_cast<int64_t>(seq) * a.heads + h0 + h) * kD + 32 * gi + 4 * g, a.dtype, v);
+            }
+            if (part && g == 0) *reinterpret_cast<float2 *>(part + 8 * NT * kD + 2 * h) = make_float2(sg.top[nt][j], l);
+        }
+}
 
 template <int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const AttnArgs a)
+constexpr int kAttnCtas = NT == 1 ? 3 : 2;  // CTAs on an SM: what their registers allow (168, or 255)
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel(const AttnArgs a)
 {
-    extern __shared__ uint8_t raw_smem[];
-    AttnSmem<NT> &sm = *reinterpret_cast<AttnSmem<NT> *>((reinterpret_cast<uintptr_t>(raw_smem) + 127) & ~uintptr_t(127));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    extern __shared__ __align__(128) uint8_t raw_smem[];
+    AttnSmem &sm = *reinterpret_cast<AttnSmem *>(raw_smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     launch_dependents();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
             const int len = a.seq_len[i];
             if (len < 0 || len > static_cast<long long>(a.max_pages) * kPage) atomicOr(a.c.err, kErrIndex);
         }
-    const int subs = a.c.heads * a.blocks;
-    const long long units = pages_before(a, a.n) * subs;
-    const long long lo = units * blockIdx.x / gridDim.x, hi = units * (blockIdx.x + 1) / gridDim.x;
-    if (lo >= hi) return;
+    const Shares s = shares_of(a);
+    // neighbouring shares go to different SMs, so that a launch with few units spreads
+    const int me = warp * gridDim.x + blockIdx.x;
+    if (me >= s.warps || s.units == 0) return;
+    const long long lo = s.begin(me), hi = s.begin(me + 1);
     const uint32_t bar0 = smem_addr(&sm.full[warp][0]), st0 = smem_addr(&sm.stage[warp][0][0]);
     if (lane == 0) {
-        for (int s = 0; s < kStagesW; ++s) barrier_init(bar0 + 8 * s, 1);
+        for (int k = 0; k < kStagesW; ++k) barrier_init(bar0 + 8 * k, 1);
         fence_barrier_init();
     }
     __syncwarp();
 
+    Walk w = place_of(a, s, lo);
     Feed feed;
-    feed.w = place_of(a, lo, subs);
-    feed.left = hi - lo;
+    feed.w = w;
+    feed.left = static_cast<int>(hi - lo);
+    feed.first = feed.end = 0;
     feed.ids = 0;
-    feed_segment(a, feed, warp);
-    Walk w = feed.w;
-    long long left = hi - lo;
-    int issued = 0, taken = 0;        // pages of this warp, by number
-    uint32_t absent = 0;              // bit s: stage s stands for a page outside the cache
-    bool dead = false;                // a copy did not arrive
+    int issued = 0, taken = 0;  // units of this warp, by number
+    uint32_t absent = 0;        // bit k: stage k stands for a half outside the cache
     const auto issue = [&]() {
-        int head = 0;
-        const int id = feed_next(a, feed, warp, subs, &head);
+        int head = 0, half = 0;
+        const int id = feed_next(a, s, feed, &head, &half);
         if (id == -1) return;
-        const int s = issued % kStagesW;
+        const int k = issued % kStagesW;
         if (id >= 0) {
-            absent &= ~(1u << s);
+            absent &= ~(1u << k);
             if (lane == 0) {
-                barrier_expect(bar0 + 8 * s, kBlock);
-                bulk_copy(st0 + s * kBlock, a.c.block(id, head), kBlock, bar0 + 8 * s);
+                const uint32_t bytes = s.shift == 2 ? kHalfBlock : kUnitBytes;
+                barrier_expect(bar0 + 8 * k, bytes);
+                bulk_copy(st0 + k * kUnitBytes, a.c.block(id, head) + half * kHalfBlock, bytes, bar0 + 8 * k);
             }
         } else {
-            absent |= 1u << s;
+            absent |= 1u << k;
             if (lane == 0) {
                 atomicOr(a.c.err, kErrIndex);
-                barrier_arrive(bar0 + 8 * s);
+                barrier_arrive(bar0 + 8 * k);
             }
         }
         ++issued;
     };
-    for (int s = 0; s < kStagesW; ++s) issue();
+    for (int k = 0; k < kStagesW; ++k) issue();
 
-    bool first = true;
-    while (left > 0) {
-        const int p0 = w.page, p1 = static_cast<int>(p0 + left < w.pages ? p0 + left : w.pages);
+    bool dead = false;  // a copy did not arrive
+    int left = static_cast<int>(hi - lo);
+    for (bool first = true; left > 0 && !dead; first = false) {
+        const int u0 = w.unit, u1 = left < w.units - u0 ? u0 + left : w.units;
         const int len = a.seq_len[w.seq];
         const int kvh = w.sub / a.blocks, hb = w.sub - kvh * a.blocks;
         const int h0 = kvh * a.group + hb * 8 * NT, nh = min(8 * NT, a.group - hb * 8 * NT);
-
-        // q as B fragments: step (group gi, j) takes dims 32 gi + 8 t + j and + 4 + j of head g, scaled by
-        // a power of two so that every row lies in binary16's range (the largest value in [1, 2))
-        uint32_t qf[NT][4][4];
-        float fac[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x[4][8], top = 0.0f;
-            const int h = nt * 8 + g;
-#pragma unroll
-            for (int gi = 0; gi < 4; ++gi) {
-                if (h < nh) load8(a.q.data, w.seq * a.q.token_stride + (h0 + h) * a.q.head_stride + 32 * gi + 8 * t, a.dtype, x[gi]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (h >= nh) x[gi][j] = 0.0f;
-                    top = fmaxf(top, fabsf(x[gi][j]));
-                }
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = top > 0.0f && top < INFINITY ? ilogbf(top) : 0;
-#pragma unroll
-            for (int gi = 0; gi < 4; ++gi)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __half2 v = __floats2half2_rn(ldexpf(x[gi][j], -e), ldexpf(x[gi][4 + j], -e));
-                    qf[nt][gi][j] = *reinterpret_cast<const uint32_t *>(&v);
-                }
-            // this head's factor is wanted where its scores are: columns 2t, 2t + 1 of every lane
-            const float f = ldexpf(a.scale_log2, e + 24);
-            fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-            fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-        }
-
-        float o[8][NT][4], top[NT][2], weight[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            top[nt][0] = top[nt][1] = -INFINITY;
-            weight[nt][0] = weight[nt][1] = 0.0f;
-#pragma unroll
-            for (int m = 0; m < 8; ++m) o[m][nt][0] = o[m][nt][1] = o[m][nt][2] = o[m][nt][3] = 0.0f;
-        }
-
-        for (int p = p0 + warp; p < p1 && !dead; p += kWarps) {
-            const int s = taken % kStagesW;
-            if (!__all_sync(0xffffffffu, barrier_wait(bar0 + 8 * s, taken / kStagesW & 1))) {
+        Segment<NT> sg;
+        begin_segment(a, sg, w.seq, h0, nh);
+        for (int u = u0; u < u1; ++u) {
+            const int k = taken % kStagesW;
+            if (!__all_sync(0xffffffffu, barrier_wait(bar0 + 8 * k, taken / kStagesW & 1))) {
                 if (lane == 0) atomicOr(a.c.err, kErrTimeout);
                 dead = true;
                 break;
             }
-            if (!(absent >> s & 1)) {
-                const uint8_t *b = sm.stage[warp][s];
-                float x[4][NT][4];
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    const int r0 = mt * 16 + g, r1 = r0 + 8;
-                    const uint4 ka = *reinterpret_cast<const uint4 *>(b + 64 * r0 + 16 * t);
-                    const uint4 kb = *reinterpret_cast<const uint4 *>(b + 64 * r1 + 16 * t);
-                    const uint2 sa = *reinterpret_cast<const uint2 *>(b + kKeyScales + 8 * r0);
-                    const uint2 sb = *reinterpret_cast<const uint2 *>(b + kKeyScales + 8 * r1);
-                    const float2 sa0 = __half22float2(*reinterpret_cast<const __half2 *>(&sa.x)), sa1 = __half22float2(*reinterpret_cast<const __half2 *>(&sa.y));
-                    const float2 sb0 = __half22float2(*reinterpret_cast<const __half2 *>(&sb.x)), sb1 = __half22float2(*reinterpret_cast<const __half2 *>(&sb.y));
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-                    const float fa[4] = {sa0.x, sa0.y, sa1.x, sa1.y}, fb[4] = {sb0.x, sb0.y, sb1.x, sb1.y};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) x[mt][nt][0] = x[mt][nt][1] = x[mt][nt][2] = x[mt][nt][3] = 0.0f;
-#pragma unroll
-                    for (int gi = 0; gi < 4; ++gi) {
-                        uint32_t pa[4], pb[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            pa[j] = pair_of(wa[gi], j);
-                            pb[j] = pair_of(wb[gi], j);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(c, pa[0], pb[0], pa[1], pb[1], qf[nt][gi][0], qf[nt][gi][1]);
-                            mma_f16(c, pa[2], pb[2], pa[3], pb[3], qf[nt][gi][2], qf[nt][gi][3]);
-                            x[mt][nt][0] = fmaf(fa[gi], c[0], x[mt][nt][0]);
-                            x[mt][nt][1] = fmaf(fa[gi], c[1], x[mt][nt][1]);
-                            x[mt][nt][2] = fmaf(fb[gi], c[2], x[mt][nt][2]);
-                            x[mt][nt][3] = fmaf(fb[gi], c[3], x[mt][nt][3]);
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[mt][nt][j] *= fac[nt][j & 1];
-                }
-                const int valid = len - p * kPage;  // tokens of this page
-                if (valid < kPage) {
-#pragma unroll
-                    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (mt * 16 + g + (j >> 1) * 8 >= valid) x[mt][nt][j] = -INFINITY;
-                }
-                // the page's largest value scale (positive binary16 values order as integers), as a power of two >= 1
-                const uint4 vs = *reinterpret_cast<const uint4 *>(b + kValueScales + 16 * lane);
-                const __half2 m2 = __hmax2(__hmax2(*reinterpret_cast<const __half2 *>(&vs.x), *reinterpret_cast<const __half2 *>(&vs.y)),
-                                           __hmax2(*reinterpret_cast<const __half2 *>(&vs.z), *reinterpret_cast<const __half2 *>(&vs.w)));
-                const uint32_t mu = *reinterpret_cast<const uint32_t *>(&m2);
-                const uint32_t biggest = __reduce_max_sync(0xffffffffu, max(mu & 0xffffu, mu >> 16));
-                const float up = static_cast<float>(max(0, static_cast<int>(biggest >> 10) - 14));
-                bool moved = false;
-                float old[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float m = -INFINITY;
-#pragma unroll
-                        for (int mt = 0; mt < 4; ++mt) m = fmaxf(m, fmaxf(x[mt][nt][j], x[mt][nt][2 + j]));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)) + up;
-                        old[nt][j] = top[nt][j];
-                        moved |= m > top[nt][j];
-                        top[nt][j] = fmaxf(top[nt][j], m);
-                    }
-                if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float f0 = exp2_approx(old[nt][0] - top[nt][0]), f1 = exp2_approx(old[nt][1] - top[nt][1]);
-                        weight[nt][0] *= f0;
-                        weight[nt][1] *= f1;
-#pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            o[m][nt][0] *= f0;
-                            o[m][nt][1] *= f1;
-                            o[m][nt][2] *= f0;
-                            o[m][nt][3] *= f1;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    const int pr = mt * 8 + t;  // pairs pr and pr + 4; both lie rotated by 2 t
-                    const int pos = (g + 2 * t & 7) * 16;
-                    const uint4 va = *reinterpret_cast<const uint4 *>(b + kValues + 128 * pr + pos);
-                    const uint4 vb = *reinterpret_cast<const uint4 *>(b + kValues + 128 * (pr + 4) + pos);
-                    const uint4 ua = *reinterpret_cast<const uint4 *>(b + kValueScales + 16 * pr);
-                    const uint4 ub = *reinterpret_cast<const uint4 *>(b + kValueScales + 16 * (pr + 4));
-                    const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-                    const uint32_t fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w};
-                    __half2 b0[NT], b1[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float e[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) e[j] = exp2_approx(x[mt][nt][j] - top[nt][j & 1] + 15.0f);
-                        weight[nt][0] += e[0] + e[2];
-                        weight[nt][1] += e[1] + e[3];
-                        const __half2 c0 = __floats2half2_rn(e[0], e[1]), c1 = __floats2half2_rn(e[2], e[3]);
-                        const uint32_t d0 = transpose8(*reinterpret_cast<const uint32_t *>(&c0));
-                        const uint32_t d1 = transpose8(*reinterpret_cast<const uint32_t *>(&c1));
-                        b0[nt] = *reinterpret_cast<const __half2 *>(&d0);
-                        b1[nt] = *reinterpret_cast<const __half2 *>(&d1);
-                    }
-#pragma unroll
-                    for (int gi = 0; gi < 4; ++gi) {
-                        uint32_t pa[4], pb[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            pa[j] = pair_of(wa[gi], j);
-                            pb[j] = pair_of(wb[gi], j);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const __half2 e0 = __hmul2(b0[nt], *reinterpret_cast<const __half2 *>(&fa[gi]));
-                            const __half2 e1 = __hmul2(b1[nt], *reinterpret_cast<const __half2 *>(&fb[gi]));
-                            const uint32_t u0 = *reinterpret_cast<const uint32_t *>(&e0), u1 = *reinterpret_cast<const uint32_t *>(&e1);
-                            mma_f16(o[2 * gi][nt], pa[0], pa[1], pb[0], pb[1], u0, u1);
-                            mma_f16(o[2 * gi + 1][nt], pa[2], pa[3], pb[2], pb[3], u0, u1);
-                        }
-                    }
+            if (!(absent >> k & 1)) {
+                const uint8_t *page = sm.stage[warp][k];
+                if (s.shift == 2) {
+                    if (u * 16 < len) take_unit<NT, 1>(sg, page, len - (u >> 1) * kHalf, u & 1);
+                } else if (u * kUnitTokens < len) {
+                    take_unit<NT, 2 * kUnit>(sg, page, len - u * kUnitTokens, 0);
                 }
             }
             __syncwarp();
             ++taken;
             issue();
         }
-
-        // join the warps in order
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float l = weight[nt][j];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (g == 0) {
-                    sm.top[warp][nt * 8 + 2 * t + j] = top[nt][j];
-                    sm.weight[warp][nt * 8 + 2 * t + j] = l;
-                }
-            }
-        __syncthreads();
-        float f[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float all = -INFINITY;
-                for (int v = 0; v < kWarps; ++v) all = fmaxf(all, sm.top[v][nt * 8 + 2 * t + j]);
-                f[nt][j] = top[nt][j] == -INFINITY ? 0.0f : exp2_approx(top[nt][j] - all);
-            }
-        for (int v = 0; v < kWarps; ++v) {
-            if (warp == v) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int m = 0; m < 8; ++m)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int dim = 32 * (m >> 1) + 4 * g + 2 * (m & 1) + (j >> 1);
-                            float *to = &sm.sum[nt * 8 + 2 * t + (j & 1)][dim];
-                            const float y = o[m][nt][j] * f[nt][j & 1];
-                            *to = v == 0 ? y : *to + y;
-                        }
-            }
-            __syncthreads();
-        }
-        const bool whole = p0 == 0 && p1 == w.pages;
-        float *part = a.part + (static_cast<size_t>(blockIdx.x) * 2 + (first ? 0 : 1)) * part_floats(NT);
-        for (int e = threadIdx.x; e < nh * kD; e += blockDim.x) {
-            const int h = e / kD, d = e - h * kD;
-            if (whole) {
-                float all = -INFINITY, l = 0.0f;
-                for (int v = 0; v < kWarps; ++v) all = fmaxf(all, sm.top[v][h]);
-                for (int v = 0; v < kWarps; ++v)
-                    if (sm.top[v][h] != -INFINITY) l += sm.weight[v][h] * exp2_approx(sm.top[v][h] - all);
-                const float y = l > 0.0f || l != l ? sm.sum[h][d] * 16777216.0f / l : 0.0f;
-                store_from_float(a.y, (static_cast<int64_t>(w.seq) * a.heads + h0 + h) * kD + d, a.dtype, y);
-            } else {
-                part[h * kD + d] = sm.sum[h][d];
-                if (d == 0) {
-                    float all = -INFINITY, l = 0.0f;
-                    for (int v = 0; v < kWarps; ++v) all = fmaxf(all, sm.top[v][h]);
-                    for (int v = 0; v < kWarps; ++v)
-                        if (sm.top[v][h] != -INFINITY) l += sm.weight[v][h] * exp2_approx(sm.top[v][h] - all);
-                    part[8 * NT * kD + 2 * h] = all;
-                    part[8 * NT * kD + 2 * h + 1] = l;
-                }
-            }
-        }
-        __syncthreads();  // the sums are read before the next segment's are written
-        first = false;
-        left -= p1 - p0;
-        next_segment(a, w, subs);
+        if (dead) break;
+        const bool whole = u0 == 0 && u1 == w.units;
+        end_segment(a, sg, w.seq, h0, nh, whole ? nullptr : a.part + (static_cast<size_t>(me) * 2 + (first ? 0 : 1)) * part_floats(NT));
+        left -= u1 - u0;
+        next_segment(a, s, w);
     }
     // after a wait that gave up, let the copies in flight land (bounded) before the memory is given back
     if (dead)
         for (; taken < issued; ++taken) barrier_wait(bar0 + 8 * (taken % kStagesW), taken / kStagesW & 1);
 }
 
-// Joins the partial sums of one (sequence, query head) in the order of the CTAs
-// that left them, and writes the zeros of sequences without tokens.  One CTA of
-// eight warps: each takes every eighth partial, a lane four dims.
+// Joins the partial sums of one (sequence, query head) in the order of the warps
+// that left them, and writes the zeros of sequences without tokens.  First the
+// factor of every partial, one a thread at a time, then the sums: a warp takes every
+// so many-th partial, a lane four dims, and the warps are added in order.
+constexpr int kMostJoinWarps = 16;
+constexpr int join_floats(int join_warps, int warps) { return join_warps * (kD + 2) + warps; }
+
 template <int NT>
-__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int ctas)
+__global__ void join_kernel(const AttnArgs a)
 {
-    __shared__ float acc[8][kD];
-    __shared__ float tops[8], weights[8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ __align__(16) float join_smem[];  // join_floats of them
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    float *acc = join_smem, *red = acc + warps * kD, *red2 = red + warps, *factor = red2 + warps;
     const int seq = blockIdx.x / a.heads, head = blockIdx.x - seq * a.heads;
     const int kvh = head / a.group, in = head - kvh * a.group, hb = in / (8 * NT), h = in - hb * 8 * NT;
-    const int subs = a.c.heads * a.blocks, sub = kvh * a.blocks + hb;
+    const Shares s = shares_of(a);
     const int len = a.seq_len[seq];
-    const int pages = pages_of(a, seq);
-    const long long units = pages_before(a, a.n) * subs;
-    const long long u0 = pages_before(a, seq) * subs + static_cast<long long>(sub) * pages, u1 = u0 + pages - 1;
+    const long long units = static_cast<long long>(pages_of(a, seq)) << s.shift;
+    const long long u0 = (pages_before(a, seq) * s.subs << s.shift) + (kvh * a.blocks + hb) * units, u1 = u0 + units - 1;
     wait_previous_grid();  // in every CTA, so that the end of this grid is the end of both
     if (len < 0 || len > static_cast<long long>(a.max_pages) * kPage) return;
     const int64_t at = (static_cast<int64_t>(seq) * a.heads + head) * kD;
     if (len == 0) {
-        if (threadIdx.x < kD) store_from_float(a.y, at + threadIdx.x, a.dtype, 0.0f);
+        for (int d = threadIdx.x; d < kD; d += blockDim.x) store_from_float(a.y, at + d, a.dtype, 0.0f);
         return;
     }
-    // CTA b has units [units b / ctas, units (b + 1) / ctas)
-    const int b0 = static_cast<int>(((u0 + 1) * ctas - 1) / units), b1 = static_cast<int>(((u1 + 1) * ctas - 1) / units);
-    if (b0 == b1) return;  // finished by one CTA
-    const auto part_of = [&](int b) {  // a segment that a CTA begins in is its first
-        const bool begins = units * b / ctas >= u0;
-        return a.part + (static_cast<size_t>(b) * 2 + (begins ? 0 : 1)) * part_floats(NT);
-    };
-    float top = -INFINITY, weight = 0.0f;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int b = b0 + warp; b <= b1; b += 8) {
-        if (units * b / ctas == units * (b + 1) / ctas) continue;  // a CTA without units
-        const float *p = part_of(b);
-        const float r = p[8 * NT * kD + 2 * h], l = p[8 * NT * kD + 2 * h + 1];
-        const float4 v = *reinterpret_cast<const float4 *>(p + h * kD + 4 * lane);
-        if (r == -INFINITY) continue;
-        const float m = fmaxf(top, r), f0 = exp2_approx(top - m), f1 = exp2_approx(r - m);
-        y = make_float4(y.x * f0 + v.x * f1, y.y * f0 + v.y * f1, y.z * f0 + v.z * f1, y.w * f0 + v.w * f1);
-        weight = weight * f0 + l * f1;
-        top = m;
+    const int w0 = s.owner(u0), count = s.owner(u1) - w0 + 1;
+    if (count == 1) return;  // one warp had all of it
+    // the segment is the last of its first warp's share unless that share begins in it, and the first of the others'
+    const int slot0 = s.begin(w0) >= u0 ? 0 : 1;
+    const auto part = [&](int i) { return a.part + (static_cast<size_t>(w0 + i) * 2 + (i == 0 ? slot0 : 0)) * part_floats(NT); };
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+        const float r = part(i)[8 * NT * kD + 2 * h];
+        factor[i] = r;
+        top = fmaxf(top, r);
     }
-    *reinterpret_cast<float4 *>(&acc[warp][4 * lane]) = y;
-    if (lane == 0) {
-        tops[warp] = top;
-        weights[warp] = weight;
-    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane == 0) red[warp] = top;
     __syncthreads();
-    if (threadIdx.x < kD) {
-        float all = -INFINITY, l = 0.0f, s = 0.0f;
-        for (int v = 0; v < 8; ++v) all = fmaxf(all, tops[v]);
-        for (int v = 0; v < 8; ++v)
-            if (tops[v] != -INFINITY) {
-                const float f = exp2_approx(tops[v] - all);
-                l += weights[v] * f;
-                s += acc[v][threadIdx.x] * f;
-            }
-        store_from_float(a.y, at + threadIdx.x, a.dtype, l > 0.0f || l != l ? s * 16777216.0f / l : 0.0f);
+    for (int v = 0; v < warps; ++v) top = fmaxf(top, red[v]);
+    float l = 0.0f;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+        const float f = factor[i] == -INFINITY ? 0.0f : exp2_approx(factor[i] - top);  // -inf: every page of it absent
+        factor[i] = f;
+        l += f * part(i)[8 * NT * kD + 2 * h + 1];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) red2[warp] = l;
+    __syncthreads();
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = warp; i < count; i += warps) {
+        const float4 v = *reinterpret_cast<const float4 *>(part(i) + h * kD + 4 * lane);
+        const float f = factor[i];
+        y = make_float4(fmaf(v.x, f, y.x), fmaf(v.y, f, y.y), fmaf(v.z, f, y.z), fmaf(v.w, f, y.w));
+    }
+    *reinterpret_cast<float4 *>(acc + warp * kD + 4 * lane) = y;
+    __syncthreads();
+    l = 0.0f;
+    for (int v = 0; v < warps; ++v) l += red2[v];
+    for (int d = threadIdx.x; d < kD; d += blockDim.x) {
+        float sum = 0.0f;
+        for (int v = 0; v < warps; ++v) sum += acc[v * kD + d];
+        store_from_float(a.y, at + d, a.dtype, l == 0.0f ? 0.0f : sum / l);
     }
 }
 
@@ -716,19 +769,19 @@ CacheView view(const stq_cache *c) { return CacheView{c->d_data, c->pages, c->he
 
 Rows rows(const stq_rows *r) { return Rows{r->data, r->token_stride, r->head_stride}; }
 
-// CTAs of one attn_decode launch: two on every SM.
-int attn_ctas(const stq_cache *c) { return 2 * c->sms; }
-
 // Blocks of 16 query heads where a key head has more than 8, else of 8.
 int attn_nt(int group) { return group > 8 ? 2 : 1; }
 
+// Warps of one attn_decode launch: all that the SMs hold.
+int attn_warps(const stq_cache *c, int nt) { return c->sms * kWarps * (nt == 1 ? kAttnCtas<1> : kAttnCtas<2>); }
+
 template <int NT>
-cudaError_t launch_attn(const AttnArgs &a, int ctas, cudaStream_t s)
+cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s)
 {
-    const int smem = static_cast<int>(sizeof(AttnSmem<NT>)) + 128;
+    const int smem = static_cast<int>(sizeof(AttnSmem));
     cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    attn_decode_kernel<NT><<<ctas, kWarps * 32, smem, s>>>(a);
+    attn_decode_kernel<NT><<<a.warps / kWarps, kWarps * 32, smem, s>>>(a);
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -738,11 +791,16 @@ cudaError_t launch_attn(const AttnArgs &a, int ctas, cudaStream_t s)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.n) * a.heads);
-    cfg.blockDim = dim3(256);
+    // a warp of the join for every four partials that an even batch leaves a segment
+    const long long partials = a.warps / std::max(1ll, static_cast<long long>(a.n) * a.c.heads * a.blocks);
+    int join_warps = 2;
+    while (join_warps < kMostJoinWarps && join_warps * 4 < partials) join_warps *= 2;
+    cfg.blockDim = dim3(join_warps * 32);
+    cfg.dynamicSmemBytes = join_floats(join_warps, a.warps) * sizeof(float);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel<NT>, a, ctas);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<NT>, a);
     count_launch();
     return e;
 }
@@ -866,7 +924,8 @@ stq_status stq_attn_decode_workspace(const stq_cache *c, int32_t n, int32_t num_
     if (n < 0) return fail_status(STQ_ERR_ARG, "n = %d", n);
     if (num_heads < 1 || num_heads % c->heads != 0)
         return fail_status(STQ_ERR_ARG, "num_heads=%d is no multiple of the cache's %d heads", num_heads, c->heads);
-    *bytes = static_cast<size_t>(stq::attn_ctas(c)) * 2 * stq::part_floats(stq::attn_nt(num_heads / c->heads)) * sizeof(float);
+    const int nt = stq::attn_nt(num_heads / c->heads);
+    *bytes = static_cast<size_t>(stq::attn_warps(c, nt)) * 2 * stq::part_floats(nt) * sizeof(float);
     return STQ_OK;
 }
 
@@ -909,9 +968,9 @@ stq_status stq_attn_decode(stq_cache *c, const int32_t *page_table, int32_t max_
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.y = y;
     a.part = static_cast<float *>(workspace);
-    const int ctas = stq::attn_ctas(c);
-    const cudaError_t e = nt == 2 ? stq::launch_attn<2>(a, ctas, static_cast<cudaStream_t>(stream))
-                                  : stq::launch_attn<1>(a, ctas, static_cast<cudaStream_t>(stream));
+    a.warps = stq::attn_warps(c, nt);
+    const cudaError_t e = nt == 2 ? stq::launch_attn<2>(a, static_cast<cudaStream_t>(stream))
+                                  : stq::launch_attn<1>(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STQ_OK : stq::cuda_fail(e, "attention launch");
 }
 

@@ -81,17 +81,37 @@ __device__ __forceinline__ float exp2_approx(float x)
 // D += A B, A 16 x 16 (row), B 16 x 8 (column), fp16 operands, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = C + A B with C given by value.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], float c0, float c1, float c2, float c3, uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// D += A B of rows 0 to 7 alone (a0, a1: the k halves of row g).
+__device__ __forceinline__ void mma_f16_rows(float (&d)[2], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1)
+{
+    asm(
+        "{\n\t.reg .f32 u, v;\n\t"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, u, v}, {%2, %4, %3, %4}, {%5, %6}, {%0, %1, %7, %7};\n\t}"
+        : "+f"(d[0]), "+f"(d[1])
+        : "r"(a0), "r"(a1), "r"(0u), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit values spread over a warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 
