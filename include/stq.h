@@ -395,6 +395,39 @@ typedef struct {
 } stq_rows;
 
 /*
+ * stq_decode_step over whole prompts, for GDN pools: entry e advances by the
+ * tokens [seq_start[e], seq_start[e + 1]) of the token arrays,
+ *   X_t = a_t X_{t-1} + b_t k_t (v_t - a_t X_{t-1}^T k_t)^T,   y_t = X_t^T q_t,
+ * with X in fp32 (sums and all) between the tokens: the page is read before the
+ * first token and quantized after the last, as stq_dequantize_state and
+ * stq_quantize_state do it.  Decoding goes on from there with stq_decode_step.
+ *   seq_start: device int32 [n + 1].  A range that is not within [0, total] or
+ *              runs backwards is taken as empty and reported (STQ_ERR_INDEX).
+ *              An empty one leaves its page as it is, or zero if fresh.
+ *   total:     tokens (rows) of the token arrays; rows of no entry are neither
+ *              read into a result nor written.
+ *   fresh:     device int32 [n], nonzero: the entry starts from the zero state
+ *              and its page's content is not read; NULL: none does.
+ *   q, k, v:   device rows of `dtype`, total tokens of num_heads heads;
+ *   beta, alpha: device fp32 [total][num_heads];
+ *   y:         device [total][num_heads][128] of `dtype`, 16-byte aligned.
+ *   state:     device fp32 [n][num_heads][128][128], 16-byte aligned: work space,
+ *              and afterwards the states after the last tokens as they were
+ *              before quantisation (of an entry that changed nothing: unspecified).
+ *   workspace: device scratch of at least stq_prompt_workspace bytes, 16-byte
+ *              aligned, owned by the caller; its content need not be kept between
+ *              calls.  Calls that may overlap on the GPU need one each, and a
+ *              state each.
+ * KDA pools (a decay for each key row) return STQ_ERR_UNSUPPORTED.
+ */
+stq_status stq_prompt_workspace(const stq_pool *pool, int32_t n, int32_t total, size_t *bytes);
+stq_status stq_prompt_step(stq_pool *pool, const int32_t *req_idx, const int32_t *slot_idx, int32_t n,
+                           const int32_t *seq_start, int32_t total, const int32_t *fresh, int32_t dtype,
+                           const stq_rows *q, const stq_rows *k, const stq_rows *v, const float *beta,
+                           const float *alpha, void *y, float *state, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
  * A cache of keys and values in 4 bits, for the softmax-attention layers of a
  * stack whose linear-attention layers keep their states in a pool.  No
  * counterpart in the paper; the codes are its symmetric absmax quantiser at

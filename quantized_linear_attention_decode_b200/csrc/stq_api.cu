@@ -636,6 +636,59 @@ stq_status stq_decode_step_split(stq_pool *p, const int32_t *req_idx, const int3
     return STQ_OK;
 }
 
+stq_status stq_prompt_workspace(const stq_pool *p, int32_t n, int32_t total, size_t *bytes)
+{
+    if (p == nullptr || bytes == nullptr) return fail(STQ_ERR_ARG, "NULL argument");
+    if (n < 0 || total < 0) return fail(STQ_ERR_ARG, "n = %d, total = %d", n, total);
+    *bytes = 256;
+    return STQ_OK;
+}
+
+stq_status stq_prompt_step(stq_pool *p, const int32_t *req_idx, const int32_t *slot_idx, int32_t n,
+                           const int32_t *seq_start, int32_t total, const int32_t *fresh, int32_t dtype,
+                           const stq_rows *q, const stq_rows *k, const stq_rows *v, const float *beta,
+                           const float *alpha, void *y, float *state, void *workspace, size_t workspace_bytes,
+                           void *stream)
+{
+    stq_status st = check_launch_args(p, req_idx, slot_idx, n);
+    if (st != STQ_OK) return st;
+    size_t need = 0;
+    st = stq_prompt_workspace(p, n, total, &need);
+    if (st != STQ_OK) return st;
+    if (p->kind != STQ_GDN) return fail(STQ_ERR_UNSUPPORTED, "prompts need a GDN pool (one decay a head and token)");
+    if (stq::dtype_bytes(dtype) == 0) return fail(STQ_ERR_ARG, "dtype %d", dtype);
+    if (q == nullptr || k == nullptr || v == nullptr) return fail(STQ_ERR_ARG, "q, k or v is NULL");
+    if (n > 0 && (seq_start == nullptr || state == nullptr || workspace == nullptr))
+        return fail(STQ_ERR_ARG, "a seq_start/state/workspace pointer is NULL");
+    if (n > 0 && total > 0 && (!q->data || !k->data || !v->data || !beta || !alpha || !y))
+        return fail(STQ_ERR_ARG, "a q/k/v/beta/alpha/y pointer is NULL");
+    if (!stq::rows_aligned(q, dtype) || !stq::rows_aligned(k, dtype) || !stq::rows_aligned(v, dtype))
+        return fail(STQ_ERR_ARG, "rows of q, k and v must start on 16-byte boundaries");
+    if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(workspace)) % 16 != 0)
+        return fail(STQ_ERR_ARG, "y, state and workspace must be 16-byte aligned");
+    if (n > 0 && workspace_bytes < need)
+        return fail(STQ_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if ((long long)n * p->H * 32 > 0x7FFFFFFFll || (long long)total * p->H > 0x7FFFFFFFll)
+        return fail(STQ_ERR_ARG, "n * H or total * H too large");
+    if (n == 0) return STQ_OK;
+    if (fault("launch")) return fail(STQ_ERR_CUDA, "injected launch failure (STQ_FAULT=launch)");
+    DeviceGuard g(p->device);
+    NvtxRange nvtx("stq_prompt_step");
+    if (!g.ok) return fail(STQ_ERR_CUDA, "cannot select device %d", p->device);
+    const cudaStream_t s0 = (cudaStream_t)stream;
+    cudaError_t e = join_async(p, s0);
+    if (e != cudaSuccess) return cuda_fail(e, "wait for the pending write-back");
+    e = debug_checks(p, req_idx, slot_idx, n, s0);
+    if (e != cudaSuccess) return cuda_fail(e, "debug checks");
+    stq::PromptIO io{req_idx, slot_idx, n, {seq_start, fresh, total}, dtype, *q, *k, *v, beta, alpha, y, state, workspace};
+    e = stq::launch_dequantize(view(p), req_idx, slot_idx, n, state, s0, io.span);
+    if (e != cudaSuccess) return cuda_fail(e, "dequantize launch");
+    e = stq::launch_prompt(view(p), io, s0);
+    if (e != cudaSuccess) return cuda_fail(e, "prompt launch");
+    e = stq::launch_quantize(view(p), req_idx, slot_idx, n, state, s0, io.span);
+    return e == cudaSuccess ? STQ_OK : cuda_fail(e, "quantize launch");
+}
+
 // ---------------------------------------------------------------- decode with built-in scratch
 //
 // The split step needs a per-tile u~ buffer between its two kernels.  Callers

@@ -83,10 +83,39 @@ cudaError_t launch_decode_writeback(const PoolView &p, const DecodeIO &io, cudaS
 // the stream) and sets kErrDuplicate in `err` for a pair named twice.
 cudaError_t launch_duplicate_check(const int32_t *req_idx, const int32_t *slot_idx, int n, int R, int S,
                                    uint32_t *seen, uint32_t *err, cudaStream_t stream);
+// Which entries of a prompt call have nothing to quantize (no token, and not begun from
+// zero) or to dequantize (begun from zero); every entry has where seq_start is NULL.
+struct PromptSpan {
+    const int32_t *seq_start = nullptr;  // [n + 1] rows of the token arrays
+    const int32_t *fresh = nullptr;      // [n], nonzero: from the zero state; NULL: none
+    int total = 0;                       // rows of the token arrays
+    __device__ bool is_fresh(int e) const { return fresh != nullptr && fresh[e] != 0; }
+    // tokens of entry e; -1 for a range that is none
+    __device__ int length(int e) const
+    {
+        const int a = seq_start[e], b = seq_start[e + 1];
+        return a < 0 || b < a || b > total ? -1 : b - a;
+    }
+};
+
 cudaError_t launch_quantize(const PoolView &p, const int32_t *req_idx, const int32_t *slot_idx,
-                            int n, const float *state, cudaStream_t stream);
+                            int n, const float *state, cudaStream_t stream, const PromptSpan &span = PromptSpan());
 cudaError_t launch_dequantize(const PoolView &p, const int32_t *req_idx, const int32_t *slot_idx,
-                              int n, float *state, cudaStream_t stream);
+                              int n, float *state, cudaStream_t stream, const PromptSpan &span = PromptSpan());
+
+// The gated delta rule over the tokens of n prompts (stq_prompt.cu).
+struct PromptIO {
+    const int32_t *req_idx, *slot_idx;
+    int n;
+    PromptSpan span;
+    int dtype;
+    stq_rows q, k, v;
+    const float *beta, *alpha;  // [total][H]
+    void *y;                    // [total][H][128] of dtype
+    float *state;               // [n][H][128][128], read (unless fresh) and written
+    void *workspace;
+};
+cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t stream);
 
 void count_launch();
 

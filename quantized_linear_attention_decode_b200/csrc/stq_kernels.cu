@@ -42,7 +42,7 @@ __device__ __forceinline__ uint8_t *tile_page(const PoolView &p, int req, int sl
 // v_ij = s_i r_i z_ij (each term formed in the oracle's operation order), and
 // stored in the page.  One warp per row.
 __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t *req_idx,
-                                                       const int32_t *slot_idx, const float *state)
+                                                       const int32_t *slot_idx, const float *state, PromptSpan span)
 {
     __shared__ double fit_sum[8][2][kD];  // per-warp column sums of the fit (num, den)
     const int tile = blockIdx.x;
@@ -52,6 +52,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
         return;
     }
+    // a prompt without tokens leaves its page as it is
+    if (span.seq_start != nullptr && span.length(ni) <= 0 && !span.is_fresh(ni)) return;
     uint8_t *page = tile_page(p, req, slot, h);
     const float *S = state + static_cast<size_t>(tile) * kD * kD;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
 // packed page -> fp32 reconstruction fl32(((s r) c) z) computed in fp64 (z: the binary16
 // value of a pivot row, without c in a fitted page).  One warp per row.
 __global__ void __launch_bounds__(256) dequantize_kernel(PoolView p, const int32_t *req_idx,
-                                                         const int32_t *slot_idx, float *state)
+                                                         const int32_t *slot_idx, float *state, PromptSpan span)
 {
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(PoolView p, const int32
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
         return;
     }
+    if (span.is_fresh(ni)) return;  // a prompt that begins from the zero state does not read its page
     const uint8_t *page = tile_page(p, req, slot, h);
     float *S = state + static_cast<size_t>(tile) * kD * kD;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(PoolView p, const int32
 // copied as fp32, and back.  256 threads, 4 consecutive elements each per step.
 template <int BITS>
 __global__ void __launch_bounds__(256) quantize_raw_kernel(PoolView p, const int32_t *req_idx,
-                                                           const int32_t *slot_idx, const float *state)
+                                                           const int32_t *slot_idx, const float *state, PromptSpan span)
 {
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
@@ -228,6 +231,8 @@ __global__ void __launch_bounds__(256) quantize_raw_kernel(PoolView p, const int
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
         return;
     }
+    // a prompt without tokens leaves its page as it is
+    if (span.seq_start != nullptr && span.length(ni) <= 0 && !span.is_fresh(ni)) return;
     uint8_t *page = tile_page(p, req, slot, h);
     const float *S = state + static_cast<size_t>(tile) * kD * kD;
     bool bad = false;
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(256) quantize_raw_kernel(PoolView p, const int
 
 template <int BITS>
 __global__ void __launch_bounds__(256) dequantize_raw_kernel(PoolView p, const int32_t *req_idx,
-                                                             const int32_t *slot_idx, float *state)
+                                                             const int32_t *slot_idx, float *state, PromptSpan span)
 {
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
@@ -260,6 +265,7 @@ __global__ void __launch_bounds__(256) dequantize_raw_kernel(PoolView p, const i
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
         return;
     }
+    if (span.is_fresh(ni)) return;  // a prompt that begins from the zero state does not read its page
     const uint8_t *page = tile_page(p, req, slot, h);
     float *S = state + static_cast<size_t>(tile) * kD * kD;
     for (int e = threadIdx.x * 4; e < kD * kD; e += 256 * 4) {
@@ -305,21 +311,21 @@ cudaError_t launch_duplicate_check(const int32_t *req_idx, const int32_t *slot_i
 }
 
 cudaError_t launch_quantize(const PoolView &p, const int32_t *req_idx, const int32_t *slot_idx,
-                            int n, const float *state, cudaStream_t stream)
+                            int n, const float *state, cudaStream_t stream, const PromptSpan &span)
 {
-    if (p.raw_bits == 32) quantize_raw_kernel<32><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state);
-    else if (p.raw_bits == 16) quantize_raw_kernel<16><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state);
-    else quantize_kernel<<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state);
+    if (p.raw_bits == 32) quantize_raw_kernel<32><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else if (p.raw_bits == 16) quantize_raw_kernel<16><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else quantize_kernel<<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     count_launch();
     return cudaGetLastError();
 }
 
 cudaError_t launch_dequantize(const PoolView &p, const int32_t *req_idx, const int32_t *slot_idx,
-                              int n, float *state, cudaStream_t stream)
+                              int n, float *state, cudaStream_t stream, const PromptSpan &span)
 {
-    if (p.raw_bits == 32) dequantize_raw_kernel<32><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state);
-    else if (p.raw_bits == 16) dequantize_raw_kernel<16><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state);
-    else dequantize_kernel<<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state);
+    if (p.raw_bits == 32) dequantize_raw_kernel<32><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else if (p.raw_bits == 16) dequantize_raw_kernel<16><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else dequantize_kernel<<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     count_launch();
     return cudaGetLastError();
 }

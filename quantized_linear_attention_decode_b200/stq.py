@@ -34,7 +34,8 @@ EXPORTS = ("stq_pool_create", "stq_pool_destroy", "stq_pool_bytes", "stq_desc_by
            "stq_export_slot", "stq_import_slot", "stq_pool_check", "stq_launch_count",
            "stq_status_str", "stq_last_error",
            "stq_cache_create", "stq_cache_destroy", "stq_cache_bytes", "stq_cache_append", "stq_cache_read",
-           "stq_attn_decode_workspace", "stq_attn_decode", "stq_cache_check")
+           "stq_attn_decode_workspace", "stq_attn_decode", "stq_cache_check",
+           "stq_prompt_workspace", "stq_prompt_step")
 
 
 class StqError(RuntimeError):
@@ -89,6 +90,8 @@ def load():
         "stq_export_slot": [P, I32, I32, P, SZ],
         "stq_import_slot": [P, I32, I32, P, SZ],
         "stq_pool_check": [P, P],
+        "stq_prompt_workspace": [P, I32, I32, P],
+        "stq_prompt_step": [P, P, P, I32, P, I32, P, I32, P, P, P, P, P, P, P, P, SZ, P],
         "stq_cache_create": [I32, I32, I32, P],
         "stq_cache_destroy": [P],
         "stq_cache_bytes": [P, P],
@@ -155,7 +158,9 @@ class Pool:
     """Owner of one stq_pool handle (destroyed with the object)."""
 
     def __init__(self, handle, kind, R, S, H, unit_bits, flags=0):
+        import torch
         self.handle = handle
+        self.device = torch.device("cuda", torch.cuda.current_device())
         self.kind, self.R, self.S, self.H = kind, R, S, H
         self.unit_bits = np.asarray(unit_bits, np.uint8).copy()
         self.flags = int(flags)
@@ -469,6 +474,37 @@ def _scratch(workspace, nbytes, device, stream):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace, workspace.numel() * workspace.element_size()
+
+
+def stq_prompt_workspace(pool: Pool, n: int, total: int) -> int:
+    """Bytes of scratch that stq_prompt_step needs for n prompts in `total` token rows."""
+    a = C.c_size_t()
+    _check(load().stq_prompt_workspace(pool.handle, int(n), int(total), C.byref(a)))
+    return a.value
+
+
+def stq_prompt_step(pool: Pool, req_idx, slot_idx, seq_start, q, k, v, beta, alpha, y, state, fresh=None, workspace=None,
+                    stream=None) -> None:
+    """stq_decode_step over whole prompts (GDN pools): entry e advances by the tokens seq_start[e]..seq_start[e + 1] of
+    q, k, v [total, H, 128] (bfloat16, float16 or float32, any token and head strides), beta, alpha [total, H] fp32, into
+    y [total, H, 128]; state fp32 [n, H, 128, 128] receives the states before they are quantized into the pool.  fresh
+    (int32 [n]) names the entries that start from the zero state."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [total, H, 128] tensor")
+    n, r, s = _idx(pool, req_idx, slot_idx)
+    total, device = int(q.shape[0]), pool.device
+    shape = (total, pool.H, 128)
+    _on(device, req_idx, slot_idx, seq_start, q, k, v, beta, alpha, y, state, fresh, workspace)
+    qr, kr, vr = (_rows(t, q, shape, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    f = torch.float32
+    work, nbytes = _scratch(workspace, stq_prompt_workspace(pool, n, total), device, stream)
+    _check(load().stq_prompt_step(
+        pool.handle, r, s, n, _dev(seq_start, torch.int32, (n + 1,), "seq_start"), total,
+        None if fresh is None else _dev(fresh, torch.int32, (n,), "fresh"), _dtype(q, "q"), C.byref(qr), C.byref(kr),
+        C.byref(vr), _dev(beta, f, (total, pool.H), "beta"), _dev(alpha, f, (total, pool.H), "alpha"),
+        _dev(y, q.dtype, shape, "y"), _dev(state, f, (n, pool.H, 128, 128), "state"), C.c_void_p(work.data_ptr()), nbytes,
+        _stream_of(stream, device)))
 
 
 class Cache:
