@@ -428,6 +428,34 @@ stq_status stq_prompt_step(stq_pool *pool, const int32_t *req_idx, const int32_t
                            void *stream);
 
 /*
+ * Causal softmax attention over packed prompts with grouped heads, for the
+ * softmax-attention layers that stand between linear ones (no counterpart in
+ * the paper).  Sequence i has the query rows [q_start[i], q_start[i + 1]) and the
+ * key rows [k_start[i], k_start[i + 1]); with Lq and Lk of them, query j sees the
+ * keys up to j + Lk - Lq (a piece of a prompt behind earlier keys; all of them
+ * new when Lq = Lk):
+ *   y[j][h] = sum_t softmax_t(scale q[j][h] . k[t][g]) v[t][g],  g = h / (num_heads / num_kv_heads).
+ * A query that sees no key (Lq > Lk) has y = 0.
+ *   q_start, k_start: device int32 [n + 1].  A range that is not within
+ *             [0, total_q] or [0, total_k], or runs backwards, is skipped (its y left
+ *             as it was) and reported.
+ *   q, k, v:  device rows of `dtype` (STQ_BF16 or STQ_F16; STQ_F32 returns
+ *             STQ_ERR_UNSUPPORTED), total_q tokens of num_heads heads and total_k of
+ *             num_kv_heads; positive strides (else STQ_ERR_UNSUPPORTED).
+ *   y:        device [total_q][num_heads][128] of `dtype`, 16-byte aligned; rows of
+ *             no sequence are left as they were.  The call runs on the device that
+ *             holds it.
+ *   err:      device int32 or NULL: receives STQ_ERR_INDEX for a bad range, or
+ *             STQ_ERR_TIMEOUT when a bounded wait gave up; else left as it is.
+ * Weights are rounded to `dtype` before they meet v; scores and sums are fp32.
+ * A sequence whose own keys or values are not all finite has unspecified
+ * results; others are not touched by it.
+ */
+stq_status stq_attn_prompt(const int32_t *q_start, const int32_t *k_start, int32_t n, int32_t num_heads,
+                           int32_t num_kv_heads, int32_t total_q, int32_t total_k, int32_t dtype, const stq_rows *q,
+                           const stq_rows *k, const stq_rows *v, float scale, void *y, int32_t *err, void *stream);
+
+/*
  * A cache of keys and values in 4 bits, for the softmax-attention layers of a
  * stack whose linear-attention layers keep their states in a pool.  No
  * counterpart in the paper; the codes are its symmetric absmax quantiser at

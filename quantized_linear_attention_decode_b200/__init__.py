@@ -15,5 +15,5 @@ from .stq import (  # noqa: F401
     stq_status_str,
     STQ_BF16, STQ_CACHE_PAGE, STQ_F16, STQ_F32, Cache, stq_attn_decode, stq_attn_decode_workspace, stq_cache_append,
     stq_cache_bytes, stq_cache_check, stq_cache_create, stq_cache_destroy, stq_cache_read,
-    stq_prompt_step, stq_prompt_workspace,
+    stq_attn_prompt, stq_prompt_step, stq_prompt_workspace,
 )

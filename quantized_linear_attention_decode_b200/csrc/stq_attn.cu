@@ -1,0 +1,495 @@
+// stq_attn.cu -- causal softmax attention over packed prompts with grouped heads (sm_100a).
+//
+//   y_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys j <= i + (Lk - Lq)
+//
+// of the query's sequence (its queries are its last Lq positions).  Bound by the
+// tensor cores, 4 x 128 operations a visible pair and head, and as much by the
+// exponentials: a 128 x 128 tile is 1024 cycles of either.
+//
+// A CTA takes 256 query rows of one key head as two tiles of 128 and walks over the
+// keys in tiles of 128.  A row is a (token, query head) pair: `pack` query heads of
+// the key head, a power of two, stand side by side, so that one key tile serves all
+// of them and a short prompt fills its tiles.  Tensor memory holds, for each query
+// tile, S = Q K^T (128 columns; its first 64 become P in 16 bits, the other operand of
+// O += P V straight from there) and O (128 columns): all 512 columns.  Warps 0-3 and
+// 4-7 do the softmax of one tile each, a thread a row: no thread needs another for
+// its maximum and sum.  Warp 8 loads (TMA, 128-byte swizzle, two stages each of K and
+// V), one lane of warp 9 issues the products: while one tile's warps take
+// exponentials, the tensor core works for the other.
+//
+// The running maximum that P is taken against moves only when a score lies more than
+// 2^8 above it (P then stays below 2^8, exact range in fp16 and bf16 alike), so O is
+// rescaled in tensor memory a few times a row and not in every tile.  P is rounded
+// to the type of v (2^-9 of a weight in bf16, as the output itself); all else is fp32.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda.h>
+
+#include "stq_host.h"
+#include "stq_tc.h"
+
+namespace stq {
+namespace {
+
+constexpr int kRows = 128;               // of a query tile, and keys of a key tile
+constexpr int kTileBytes = kRows * kD * 2;
+constexpr int kHalfTile = kTileBytes / 2;  // 64 of the 128 dims: rows of 128 bytes
+constexpr int kStages = 2;
+constexpr int kThreads = 384;  // three warpgroups; warps 10 and 11 only hand their registers over
+// registers a thread: 168 at launch, then 216 in the softmax warpgroups and 72 in the third (2 * 216 + 72 = 3 * 168)
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+
+struct PromptAttn {
+    const int32_t *q_start, *k_start;
+    int n, heads, group, pack, total_q, total_k;
+    float scale_log2;  // |scale| log2(e)
+    bool negative;     // scale < 0
+    void *y;
+    int32_t *err;
+};
+
+struct __align__(1024) AttnSmem {
+    uint8_t q[2][kTileBytes];
+    uint8_t k[kStages][kTileBytes], v[kStages][kTileBytes];
+    unsigned long long q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    unsigned long long s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    int item[8];  // sequence's first query row, its queries, first key row, keys, this CTA's first token, first head, key head
+};
+
+// Queries and keys of sequence i; false where a range is none.
+__device__ __forceinline__ bool sequence(const PromptAttn &a, int i, int *lq, int *lk)
+{
+    const int q0 = a.q_start[i], q1 = a.q_start[i + 1], k0 = a.k_start[i], k1 = a.k_start[i + 1];
+    *lq = q1 - q0;
+    *lk = k1 - k0;
+    return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
+}
+
+// The CTA's sequence and tokens: tiles of all sequences in order, within a sequence from its end, where
+// a tile sees most keys.  One warp; false when there is no such tile.
+__device__ __forceinline__ bool find_item(const PromptAttn &a, int tile, int *seq, int *token)
+{
+    const int lane = threadIdx.x & 31, tokens = 2 * kRows / a.pack;
+    long long base = 0;
+    for (int first = 0; first < a.n; first += 32) {
+        int lq = 0, lk, mine = 0;
+        if (first + lane < a.n && sequence(a, first + lane, &lq, &lk)) mine = (lq + tokens - 1) / tokens;
+        long long upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, base + upto > tile);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            const long long end = base + __shfl_sync(0xffffffffu, upto, who);
+            *seq = first + who;
+            *token = static_cast<int>(end - 1 - tile) * tokens;
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+__device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
+
+// Two values in the 16-bit type of v.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if (BF16) {
+        const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&w);
+    }
+    const __half2 w = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&w);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, const PromptAttn a)
+{
+    extern __shared__ uint8_t raw_smem[];
+    AttnSmem &sm = *reinterpret_cast<AttnSmem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && a.err != nullptr)
+        for (int i = threadIdx.x; i < a.n; i += kThreads) {
+            int lq, lk;
+            if (!sequence(a, i, &lq, &lk)) *a.err = STQ_ERR_INDEX;
+        }
+    if (warp == 0) {
+        int seq = 0, token = 0;
+        const bool found = find_item(a, blockIdx.x, &seq, &token);
+        if (lane == 0) {
+            sm.item[0] = found ? a.q_start[seq] : -1;
+            if (found) {
+                sm.item[1] = a.q_start[seq + 1] - a.q_start[seq];
+                sm.item[2] = a.k_start[seq];
+                sm.item[3] = a.k_start[seq + 1] - a.k_start[seq];
+                sm.item[4] = token;
+            }
+        }
+    } else if (warp == 8 && lane == 0) {
+        barrier_init(smem_addr(&sm.q_full), 1);
+        for (int s = 0; s < kStages; ++s) {
+            barrier_init(smem_addr(&sm.k_full[s]), 1);
+            barrier_init(smem_addr(&sm.k_empty[s]), 1);
+            barrier_init(smem_addr(&sm.v_full[s]), 1);
+            barrier_init(smem_addr(&sm.v_empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(smem_addr(&sm.s_full[i]), 1);
+            barrier_init(smem_addr(&sm.p_full[i]), kRows);
+            barrier_init(smem_addr(&sm.o_full[i]), 1);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const int q_row0 = sm.item[0], lq = sm.item[1], k_row0 = sm.item[2], lk = sm.item[3], token0 = sm.item[4];
+    if (q_row0 < 0) return;
+    // blockIdx.y: key head and block of `pack` query heads
+    const int blocks = a.group / a.pack, kv_head = blockIdx.y / blocks, head0 = blockIdx.y * a.pack;
+    const int per_tile = kRows / a.pack;  // tokens of a query tile
+    // key tiles of each query tile: up to what its last token sees
+    int tiles[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int first = token0 + i * per_tile, last = min(first + per_tile, lq) - 1;
+        const int seen = first < lq ? min(lk, last + lk - lq + 1) : 0;
+        tiles[i] = seen > 0 ? (seen + kRows - 1) / kRows : 0;
+    }
+    const int all = max(tiles[0], tiles[1]);
+    if (warp == 9) tmem_alloc(smem_addr(&sm.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    bool ok = true;
+
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+
+    if (warp == 8) {
+        if (lane == 0 && all > 0) {
+            const uint32_t qf = smem_addr(&sm.q_full);
+            barrier_expect(qf, (tiles[0] > 0 ? kTileBytes : 0) + (tiles[1] > 0 ? kTileBytes : 0));
+            for (int i = 0; i < 2; ++i)
+                for (int half = 0; half < 2 && tiles[i] > 0; ++half)
+                    tma_load3(smem_addr(sm.q[i]) + half * kHalfTile, &q_map, qf, 64 * half, head0, q_row0 + token0 + i * per_tile);
+            int issued = 0;
+            for (int j = 0; j < all && ok; ++j, ++issued) {
+                const int s = j % kStages;
+                const uint32_t parity = (j / kStages & 1) ^ 1;
+                const uint32_t kf = smem_addr(&sm.k_full[s]), vf = smem_addr(&sm.v_full[s]);
+                ok = j < kStages || barrier_wait(smem_addr(&sm.k_empty[s]), parity);
+                if (!ok) break;
+                barrier_expect(kf, kTileBytes);
+                for (int half = 0; half < 2; ++half)
+                    tma_load3(smem_addr(sm.k[s]) + half * kHalfTile, &k_map, kf, 64 * half, kv_head, k_row0 + j * kRows);
+                ok = j < kStages || barrier_wait(smem_addr(&sm.v_empty[s]), parity);
+                barrier_expect(vf, kTileBytes);
+                for (int half = 0; half < 2; ++half)
+                    tma_load3(smem_addr(sm.v[s]) + half * kHalfTile, &v_map, vf, 64 * half, kv_head, k_row0 + j * kRows);
+            }
+            if (!ok) {  // the loads in flight land before the memory is given back
+                barrier_wait(qf, 0);
+                for (int j = max(0, issued - kStages); j < issued; ++j) {
+                    barrier_wait(smem_addr(&sm.k_full[j % kStages]), j / kStages & 1);
+                    barrier_wait(smem_addr(&sm.v_full[j % kStages]), j / kStages & 1);
+                }
+            }
+        }
+    } else if (warp == 9) {
+        constexpr uint32_t type = BF16 ? 1 : 0;
+        const uint32_t qk = tc_idesc(type, kRows, kRows, false, false) | (a.negative ? 1u << 13 : 0u);
+        constexpr uint32_t pv = tc_idesc(type, kRows, kD, true);
+        const auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
+            if (lane == 0) {
+                const uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[j % kStages]);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t off = (s >> 2) * kHalfTile + (s & 3) * 32;
+                    tc_mma_ss(tmem + 128 * i, tc_desc(qa + off, 16, 1024), tc_desc(ka + off, 16, 1024), qk, s > 0);
+                }
+                tc_commit(smem_addr(&sm.s_full[i]));
+            }
+            __syncwarp();
+        };
+        if (all > 0) ok = barrier_wait(smem_addr(&sm.q_full), 0) && barrier_wait(smem_addr(&sm.k_full[0]), 0);
+        if (ok && all > 0) {
+            tc_fence_after();
+            for (int i = 0; i < 2; ++i)
+                if (tiles[i] > 0) scores(i, 0);
+            if (lane == 0) tc_commit(smem_addr(&sm.k_empty[0]));
+        }
+        for (int j = 0; j < all && ok; ++j) {
+            const int s = j % kStages;
+            ok = barrier_wait(smem_addr(&sm.v_full[s]), j / kStages & 1);
+            if (!ok) break;
+            const int valid = lk - j * kRows;
+            if (valid < kRows) {
+                // rows behind the sequence's last key are another sequence's or nobody's: their weights are zero,
+                // but zero times an infinity is not
+                for (int e = lane; e < (kRows - valid) * 8; e += 32)
+                    for (int half = 0; half < 2; ++half)
+                        *reinterpret_cast<uint4 *>(sm.v[s] + half * kHalfTile + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+            for (int i = 0; i < 2 && ok; ++i) {
+                if (j >= tiles[i]) continue;
+                ok = barrier_wait(smem_addr(&sm.p_full[i]), j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t va = smem_addr(sm.v[s]);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
+                    tc_commit(smem_addr(&sm.o_full[i]));
+                }
+                __syncwarp();
+                if (j + 1 < tiles[i]) {  // the next scores go where P is: after the product that reads it
+                    ok = barrier_wait(smem_addr(&sm.k_full[(j + 1) % kStages]), (j + 1) / kStages & 1) &&
+                         barrier_wait(smem_addr(&sm.o_full[i]), j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(i, j + 1);
+                }
+            }
+            if (ok && lane == 0) {
+                tc_commit(smem_addr(&sm.v_empty[s]));
+                if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[(j + 1) % kStages]));
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) {  // products in flight end before the memory is given back
+            tc_commit(smem_addr(&sm.q_full));
+            barrier_wait(smem_addr(&sm.q_full), 1);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + 128 * i + lanes, to = tmem + 256 + 128 * i + lanes;
+        const int token = token0 + i * per_tile + row / a.pack;
+        const int sees = min(lk, token + lk - lq + 1);  // keys that this row sees (none: <= 0)
+        const int least = min(lk, token0 + i * per_tile + lk - lq + 1);  // that the tile's first row sees
+        const float c = a.scale_log2;
+        float top = -INFINITY, sum = 0.0f;  // in units of log 2: P = exp2(c s - top)
+        for (int j = 0; j < tiles[i] && ok; ++j) {
+            ok = barrier_wait(smem_addr(&sm.s_full[i]), j & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_load32(ts + 32 * b, x[b]);
+            tmem_wait_load();
+            if ((j + 1) * kRows > least) {
+                const int limit = sees - j * kRows;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * b + e >= limit) x[b][e] = 0xff800000u;
+            }
+            float m = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) m = fmaxf(m, fmaxf(f_of(x[b][e]), f_of(x[b][e + 1])));
+            m *= c;
+            const bool moves = m > top + 8.0f;
+            if (__any_sync(0xffffffffu, moves)) {
+                const float now = moves ? m : top;
+                const float f = top == -INFINITY ? 0.0f : exp2_approx(top - now);
+                top = now;
+                sum *= f;
+                if (j > 0) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t o[32];
+                        tmem_load32(to + 32 * b, o);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f_of(o[e]) * f);
+                        tmem_store32(to + 32 * b, o);
+                    }
+                }
+            }
+            const float off = top == -INFINITY ? 0.0f : -top;
+            float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const uint32_t *s = &x[2 * b + (e >> 4)][2 * (e & 15)];
+                    float2 z = __ffma2_rn(make_float2(f_of(s[0]), f_of(s[1])), make_float2(c, c), make_float2(off, off));
+                    z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                    part = __fadd2_rn(part, z);
+                    w[e] = pack2<BF16>(z.x, z.y);
+                }
+                tmem_store32(ts + 32 * b, w);
+            }
+            sum += part.x + part.y;
+            tmem_wait_store();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.p_full[i]));
+        }
+        if (ok && tiles[i] > 0) ok = barrier_wait(smem_addr(&sm.o_full[i]), (tiles[i] - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tc_fence_after();
+            const float f = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that sees no key is zero
+            uint16_t *y = static_cast<uint16_t *>(a.y) + (static_cast<int64_t>(q_row0 + token) * a.heads + head0 + row % a.pack) * kD;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t o[32];
+                if (tiles[i] > 0) {
+                    tmem_load32(to + 32 * b, o);
+                    tmem_wait_load();
+                }
+                if (token < lq) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            w[d] = f == 0.0f ? 0u : pack2<BF16>(f_of(o[8 * e + 2 * d]) * f, f_of(o[8 * e + 2 * d + 1]) * f);
+                        *reinterpret_cast<uint4 *>(y + 32 * b + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+    if (!ok && a.err != nullptr) *a.err = STQ_ERR_TIMEOUT;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// cuTensorMapEncodeTiled, from the driver that the runtime has loaded.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// Rows [tokens][heads][128] in boxes of 64 dims x `box_heads` heads x `box_tokens` tokens.
+bool make_map(CUtensorMap *map, const stq_rows *r, int32_t dtype, int tokens, int heads, int box_heads, int box_tokens)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return false;
+    // a dimension of one element has no stride; the map wants some valid one
+    const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? r->head_stride : kD) * 2,
+                                   static_cast<cuuint64_t>(tokens > 1 ? r->token_stride : kD) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode(map, dtype == STQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void *>(r->data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+stq_status check_rows(const stq_rows *r, const char *name, int32_t dtype, int32_t heads, int32_t tokens)
+{
+    if (r == nullptr) return fail_status(STQ_ERR_ARG, "%s is NULL", name);
+    if (tokens > 0 && r->data == nullptr) return fail_status(STQ_ERR_ARG, "%s.data is NULL", name);
+    if (!rows_aligned(r, dtype)) return fail_status(STQ_ERR_ARG, "%s: rows must start on 16-byte boundaries", name);
+    const int64_t most = int64_t(1) << 38;
+    if ((heads > 1 && (r->head_stride <= 0 || r->head_stride >= most)) || (tokens > 1 && (r->token_stride <= 0 || r->token_stride >= most)))
+        return fail_status(STQ_ERR_UNSUPPORTED, "%s: strides must be positive (and below 2^38)", name);
+    return STQ_OK;
+}
+
+}  // namespace
+}  // namespace stq
+
+using stq::fail_status;
+
+extern "C" stq_status stq_attn_prompt(const int32_t *q_start, const int32_t *k_start, int32_t n, int32_t num_heads,
+                                      int32_t num_kv_heads, int32_t total_q, int32_t total_k, int32_t dtype,
+                                      const stq_rows *q, const stq_rows *k, const stq_rows *v, float scale, void *y,
+                                      int32_t *err, void *stream)
+{
+    if (n < 0 || total_q < 0 || total_k < 0) return fail_status(STQ_ERR_ARG, "n = %d, total_q = %d, total_k = %d", n, total_q, total_k);
+    if (num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads != 0)
+        return fail_status(STQ_ERR_ARG, "num_heads=%d is no multiple of num_kv_heads=%d", num_heads, num_kv_heads);
+    if (stq::dtype_bytes(dtype) == 0) return fail_status(STQ_ERR_ARG, "dtype %d", dtype);
+    if (dtype == STQ_F32) return fail_status(STQ_ERR_UNSUPPORTED, "prompt attention takes 16-bit types");
+    if (!std::isfinite(scale)) return fail_status(STQ_ERR_ARG, "scale is not finite");
+    stq_status st = stq::check_rows(q, "q", dtype, num_heads, total_q);
+    if (st == STQ_OK) st = stq::check_rows(k, "k", dtype, num_kv_heads, total_k);
+    if (st == STQ_OK) st = stq::check_rows(v, "v", dtype, num_kv_heads, total_k);
+    if (st != STQ_OK) return st;
+    if (n > 0 && (q_start == nullptr || k_start == nullptr)) return fail_status(STQ_ERR_ARG, "q_start or k_start is NULL");
+    if (n > 0 && total_q > 0 && y == nullptr) return fail_status(STQ_ERR_ARG, "y is NULL");
+    if (reinterpret_cast<uintptr_t>(y) % 16 != 0) return fail_status(STQ_ERR_ARG, "y must be 16-byte aligned");
+    const int group = num_heads / num_kv_heads;
+    int pack = 1;  // the largest power of two that divides the group, up to a tile's rows
+    while (pack < stq::kRows && group % (2 * pack) == 0) pack *= 2;
+    const long long tiles = (static_cast<long long>(total_q) * pack + 2 * stq::kRows - 1) / (2 * stq::kRows) + n;
+    if (tiles > 0x7FFFFFFFll || num_heads / pack > 65535) return fail_status(STQ_ERR_ARG, "too many query tiles or heads");
+    if (n == 0 || total_q == 0) return STQ_OK;
+    if (stq::fault("launch")) return fail_status(STQ_ERR_CUDA, "injected launch failure (STQ_FAULT=launch)");
+    cudaPointerAttributes where;
+    cudaError_t e = cudaPointerGetAttributes(&where, y);
+    if (e != cudaSuccess) return stq::cuda_fail(e, "device of y");
+    if (where.type != cudaMemoryTypeDevice && where.type != cudaMemoryTypeManaged) return fail_status(STQ_ERR_ARG, "y is no device memory");
+    stq::DeviceGuard g(where.device);
+    stq::NvtxRange nvtx("stq_attn_prompt");
+    if (!g.ok) return fail_status(STQ_ERR_CUDA, "cannot select device %d", where.device);
+    CUtensorMap qm, km, vm;
+    // without any key the maps of k and v are not used: q's stand in
+    const stq_rows *kr = total_k > 0 ? k : q, *vr = total_k > 0 ? v : q;
+    const int kt = total_k > 0 ? total_k : total_q, kh = total_k > 0 ? num_kv_heads : num_heads;
+    if (!stq::make_map(&qm, q, dtype, total_q, num_heads, pack, stq::kRows / pack) ||
+        !stq::make_map(&km, kr, dtype, kt, kh, 1, stq::kRows) || !stq::make_map(&vm, vr, dtype, kt, kh, 1, stq::kRows))
+        return fail_status(STQ_ERR_CUDA, "tensor map");
+    stq::PromptAttn a;
+    a.q_start = q_start;
+    a.k_start = k_start;
+    a.n = n;
+    a.heads = num_heads;
+    a.group = group;
+    a.pack = pack;
+    a.total_q = total_q;
+    a.total_k = total_k;
+    // at least 2^-100, so that a hidden score of -inf stays one
+    a.scale_log2 = static_cast<float>(std::max(std::fabs(static_cast<double>(scale)) * 1.4426950408889634, 0x1p-100));
+    a.negative = scale < 0.0f;
+    a.y = y;
+    a.err = err;
+    const auto kernel = dtype == STQ_BF16 ? stq::attn_prompt_kernel<true> : stq::attn_prompt_kernel<false>;
+    const int smem = static_cast<int>(sizeof(stq::AttnSmem)) + 1024;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return stq::cuda_fail(e, "prompt attention attribute");
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(num_heads / pack));
+    kernel<<<grid, stq::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(qm, km, vm, a);
+    stq::count_launch();
+    e = cudaGetLastError();
+    return e == cudaSuccess ? STQ_OK : stq::cuda_fail(e, "prompt attention launch");
+}

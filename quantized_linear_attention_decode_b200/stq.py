@@ -35,7 +35,7 @@ EXPORTS = ("stq_pool_create", "stq_pool_destroy", "stq_pool_bytes", "stq_desc_by
            "stq_status_str", "stq_last_error",
            "stq_cache_create", "stq_cache_destroy", "stq_cache_bytes", "stq_cache_append", "stq_cache_read",
            "stq_attn_decode_workspace", "stq_attn_decode", "stq_cache_check",
-           "stq_prompt_workspace", "stq_prompt_step")
+           "stq_prompt_workspace", "stq_prompt_step", "stq_attn_prompt")
 
 
 class StqError(RuntimeError):
@@ -92,6 +92,7 @@ def load():
         "stq_pool_check": [P, P],
         "stq_prompt_workspace": [P, I32, I32, P],
         "stq_prompt_step": [P, P, P, I32, P, I32, P, I32, P, P, P, P, P, P, P, P, SZ, P],
+        "stq_attn_prompt": [P, P, I32, I32, I32, I32, I32, I32, P, P, P, C.c_float, P, P, P],
         "stq_cache_create": [I32, I32, I32, P],
         "stq_cache_destroy": [P],
         "stq_cache_bytes": [P, P],
@@ -504,6 +505,29 @@ def stq_prompt_step(pool: Pool, req_idx, slot_idx, seq_start, q, k, v, beta, alp
         None if fresh is None else _dev(fresh, torch.int32, (n,), "fresh"), _dtype(q, "q"), C.byref(qr), C.byref(kr),
         C.byref(vr), _dev(beta, f, (total, pool.H), "beta"), _dev(alpha, f, (total, pool.H), "alpha"),
         _dev(y, q.dtype, shape, "y"), _dev(state, f, (n, pool.H, 128, 128), "state"), C.c_void_p(work.data_ptr()), nbytes,
+        _stream_of(stream, device)))
+
+
+def stq_attn_prompt(q_start, k_start, q, k, v, y, scale=None, err=None, stream=None) -> None:
+    """Causal softmax attention over packed prompts: q, y [total_q, num_heads, 128], k, v [total_k, num_kv_heads, 128]
+    (bfloat16 or float16), q_start and k_start int32 [n + 1]; the queries of a sequence are its last positions.  scale
+    defaults to 1 / sqrt(128); err (int32 [1], zeroed by the caller) receives a device-side status."""
+    import torch
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a [tokens, heads, 128] tensor")
+    n = int(q_start.numel()) - 1
+    if n < 0:
+        raise ValueError("q_start must have n + 1 entries")
+    device = q.device
+    _on(device, q_start, k_start, k, v, y, err)
+    tq, heads, tk, kv = int(q.shape[0]), int(q.shape[1]), int(k.shape[0]), int(k.shape[1])
+    qr, kr, vr = _rows(q, q, (tq, heads, 128), "q"), _rows(k, q, (tk, kv, 128), "k"), _rows(v, q, (tk, kv, 128), "v")
+    i32 = torch.int32
+    _check(load().stq_attn_prompt(
+        _dev(q_start, i32, (n + 1,), "q_start"), _dev(k_start, i32, (n + 1,), "k_start"), n, heads, kv, tq, tk,
+        _dtype(q, "q"), C.byref(qr), C.byref(kr), C.byref(vr), 128 ** -0.5 if scale is None else float(scale),
+        _dev(y, q.dtype, (tq, heads, 128), "y"), None if err is None else _dev(err, i32, (1,), "err"),
         _stream_of(stream, device)))
 
 
