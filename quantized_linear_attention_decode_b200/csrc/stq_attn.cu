@@ -95,6 +95,13 @@ __device__ __forceinline__ bool find_item(const PromptAttn &a, int tile, int *se
     return false;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
 
 // Two values in the 16-bit type of v.
@@ -171,11 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem;
     bool ok = true;
 
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-
-    if (warp == 8) {
-        if (lane == 0 && all > 0) {
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8 && lane == 0 && all > 0) {
             const uint32_t qf = smem_addr(&sm.q_full);
             barrier_expect(qf, (tiles[0] > 0 ? kTileBytes : 0) + (tiles[1] > 0 ? kTileBytes : 0));
             for (int i = 0; i < 2; ++i)
@@ -204,76 +209,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == 9) {
-        constexpr uint32_t type = BF16 ? 1 : 0;
-        const uint32_t qk = tc_idesc(type, kRows, kRows, false, false) | (a.negative ? 1u << 13 : 0u);
-        constexpr uint32_t pv = tc_idesc(type, kRows, kD, true);
-        const auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-            if (lane == 0) {
-                const uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[j % kStages]);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t off = (s >> 2) * kHalfTile + (s & 3) * 32;
-                    tc_mma_ss(tmem + 128 * i, tc_desc(qa + off, 16, 1024), tc_desc(ka + off, 16, 1024), qk, s > 0);
-                }
-                tc_commit(smem_addr(&sm.s_full[i]));
-            }
-            __syncwarp();
-        };
-        if (all > 0) ok = barrier_wait(smem_addr(&sm.q_full), 0) && barrier_wait(smem_addr(&sm.k_full[0]), 0);
-        if (ok && all > 0) {
-            tc_fence_after();
-            for (int i = 0; i < 2; ++i)
-                if (tiles[i] > 0) scores(i, 0);
-            if (lane == 0) tc_commit(smem_addr(&sm.k_empty[0]));
-        }
-        for (int j = 0; j < all && ok; ++j) {
-            const int s = j % kStages;
-            ok = barrier_wait(smem_addr(&sm.v_full[s]), j / kStages & 1);
-            if (!ok) break;
-            const int valid = lk - j * kRows;
-            if (valid < kRows) {
-                // rows behind the sequence's last key are another sequence's or nobody's: their weights are zero,
-                // but zero times an infinity is not
-                for (int e = lane; e < (kRows - valid) * 8; e += 32)
-                    for (int half = 0; half < 2; ++half)
-                        *reinterpret_cast<uint4 *>(sm.v[s] + half * kHalfTile + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                __syncwarp();
-            }
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (j >= tiles[i]) continue;
-                ok = barrier_wait(smem_addr(&sm.p_full[i]), j & 1);
-                if (!ok) break;
-                tc_fence_after();
+        if (warp == 9) {
+            constexpr uint32_t type = BF16 ? 1 : 0;
+            const uint32_t qk = tc_idesc(type, kRows, kRows, false, false) | (a.negative ? 1u << 13 : 0u);
+            constexpr uint32_t pv = tc_idesc(type, kRows, kD, true);
+            const auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
                 if (lane == 0) {
-                    const uint32_t va = smem_addr(sm.v[s]);
+                    const uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[j % kStages]);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
-                    tc_commit(smem_addr(&sm.o_full[i]));
+                    for (int s = 0; s < 8; ++s) {
+                        const uint32_t off = (s >> 2) * kHalfTile + (s & 3) * 32;
+                        tc_mma_ss(tmem + 128 * i, tc_desc(qa + off, 16, 1024), tc_desc(ka + off, 16, 1024), qk, s > 0);
+                    }
+                    tc_commit(smem_addr(&sm.s_full[i]));
                 }
                 __syncwarp();
-                if (j + 1 < tiles[i]) {  // the next scores go where P is: after the product that reads it
-                    ok = barrier_wait(smem_addr(&sm.k_full[(j + 1) % kStages]), (j + 1) / kStages & 1) &&
-                         barrier_wait(smem_addr(&sm.o_full[i]), j & 1);
+            };
+            if (all > 0) ok = barrier_wait(smem_addr(&sm.q_full), 0) && barrier_wait(smem_addr(&sm.k_full[0]), 0);
+            if (ok && all > 0) {
+                tc_fence_after();
+                for (int i = 0; i < 2; ++i)
+                    if (tiles[i] > 0) scores(i, 0);
+                if (lane == 0) tc_commit(smem_addr(&sm.k_empty[0]));
+            }
+            for (int j = 0; j < all && ok; ++j) {
+                const int s = j % kStages;
+                ok = barrier_wait(smem_addr(&sm.v_full[s]), j / kStages & 1);
+                if (!ok) break;
+                const int valid = lk - j * kRows;
+                if (valid < kRows) {
+                    // rows behind the sequence's last key are another sequence's or nobody's: their weights are zero,
+                    // but zero times an infinity is not
+                    for (int e = lane; e < (kRows - valid) * 8; e += 32)
+                        for (int half = 0; half < 2; ++half)
+                            *reinterpret_cast<uint4 *>(sm.v[s] + half * kHalfTile + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                for (int i = 0; i < 2 && ok; ++i) {
+                    if (j >= tiles[i]) continue;
+                    ok = barrier_wait(smem_addr(&sm.p_full[i]), j & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(i, j + 1);
+                    if (lane == 0) {
+                        const uint32_t va = smem_addr(sm.v[s]);
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)
+                            tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
+                        tc_commit(smem_addr(&sm.o_full[i]));
+                    }
+                    __syncwarp();
+                    if (j + 1 < tiles[i]) {  // the next scores go where P is: after the product that reads it
+                        ok = barrier_wait(smem_addr(&sm.k_full[(j + 1) % kStages]), (j + 1) / kStages & 1) &&
+                             barrier_wait(smem_addr(&sm.o_full[i]), j & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(i, j + 1);
+                    }
                 }
+                if (ok && lane == 0) {
+                    tc_commit(smem_addr(&sm.v_empty[s]));
+                    if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[(j + 1) % kStages]));
+                }
+                __syncwarp();
             }
-            if (ok && lane == 0) {
-                tc_commit(smem_addr(&sm.v_empty[s]));
-                if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[(j + 1) % kStages]));
+            if (!ok && lane == 0) {  // products in flight end before the memory is given back
+                tc_commit(smem_addr(&sm.q_full));
+                barrier_wait(smem_addr(&sm.q_full), 1);
             }
             __syncwarp();
         }
-        if (!ok && lane == 0) {  // products in flight end before the memory is given back
-            tc_commit(smem_addr(&sm.q_full));
-            barrier_wait(smem_addr(&sm.q_full), 1);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int i = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * i + lanes, to = tmem + 256 + 128 * i + lanes;
@@ -289,24 +296,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            uint32_t x[4][32];
+            // the second half of the keys first, for its maximum alone; then the first half, which stays; P takes the
+            // place of the first half's columns, so the second half is still there to be read again
+            const int limit = (j + 1) * kRows > least ? sees - j * kRows : kRows;
+            uint32_t x[2][32];
+            const auto fetch = [&](int half) {
+                tmem_load32(ts + 64 * half, x[0]);
+                tmem_load32(ts + 64 * half + 32, x[1]);
+                tmem_wait_load();
+                if ((j + 1) * kRows > least) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_load32(ts + 32 * b, x[b]);
-            tmem_wait_load();
-            if ((j + 1) * kRows > least) {
-                const int limit = sees - j * kRows;
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                        for (int e = 0; e < 32; ++e)
+                            if (64 * half + 32 * b + e >= limit) x[b][e] = 0xff800000u;
+                }
+            };
+            const auto largest = [&](float m) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * b + e >= limit) x[b][e] = 0xff800000u;
-            }
-            float m = -INFINITY;
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) m = fmaxf(m, fmaxf(f_of(x[b][e]), f_of(x[b][e + 1])));
-            m *= c;
+                    for (int e = 0; e < 32; e += 2) m = max3(m, f_of(x[b][e]), f_of(x[b][e + 1]));
+                return m;
+            };
+            fetch(1);
+            float m = largest(-INFINITY);
+            fetch(0);
+            m = largest(m) * c;
             const bool moves = m > top + 8.0f;
             if (__any_sync(0xffffffffu, moves)) {
                 const float now = moves ? m : top;
@@ -328,17 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float off = top == -INFINITY ? 0.0f : -top;
             float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int half = 0; half < 2; ++half) {
+                if (half == 1) fetch(1);
                 uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const uint32_t *s = &x[2 * b + (e >> 4)][2 * (e & 15)];
+                    const uint32_t *s = &x[e >> 4][2 * (e & 15)];
                     float2 z = __ffma2_rn(make_float2(f_of(s[0]), f_of(s[1])), make_float2(c, c), make_float2(off, off));
                     z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
                     part = __fadd2_rn(part, z);
                     w[e] = pack2<BF16>(z.x, z.y);
                 }
-                tmem_store32(ts + 32 * b, w);
+                tmem_store32(ts + 32 * half, w);
             }
             sum += part.x + part.y;
             tmem_wait_store();
