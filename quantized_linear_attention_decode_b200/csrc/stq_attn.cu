@@ -23,6 +23,7 @@
 // to the type of v (2^-9 of a weight in bf16, as the output itself); all else is fp32.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -53,7 +54,7 @@ struct __align__(1024) AttnSmem {
     uint8_t q[2][kTileBytes];
     uint8_t k[kStages][kTileBytes], v[kStages][kTileBytes];
     unsigned long long q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    unsigned long long s_full[2], p_full[2], o_full[2];
+    unsigned long long s_full[2], p_full[2][2], o_full[2];  // p_full: of either half of the keys
     uint32_t tmem;
     int item[8];  // sequence's first query row, its queries, first key row, keys, this CTA's first token, first head, key head
 };
@@ -104,6 +105,27 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 
 __device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
 
+// Of eight pairs of exponentials, how many are computed on the fp32 pipe: the special-function unit
+// takes 1024 cycles for a tile's, as long as the tensor core for its products.
+constexpr int kPolynomial = 3;
+
+// 2^x of a pair, x <= 2^7 (2^-126 where x is less, so not for hidden keys): x = n + f with n the nearest integer (by adding 1.5 2^23), 2^f by a polynomial of
+// degree 4 fitted at the Chebyshev nodes of [-1/2, 1/2] (relative error below 4e-6, a hundredth of what
+// rounding P to fp16 costs), n added to the exponent.
+__device__ __forceinline__ float2 exp2_polynomial(float2 x)
+{
+    x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
+    const float2 big = make_float2(12582912.0f, 12582912.0f);
+    const float2 r = __fadd2_rn(x, big);
+    const float2 f = __fadd2_rn(x, __fadd2_rn(big, make_float2(-r.x, -r.y)));
+    float2 p = __ffma2_rn(f, make_float2(0.00966637f, 0.00966637f), make_float2(0.05592198f, 0.05592198f));
+    p = __ffma2_rn(p, f, make_float2(0.24022349f, 0.24022349f));
+    p = __ffma2_rn(p, f, make_float2(0.69312105f, 0.69312105f));
+    p = __ffma2_rn(p, f, make_float2(1.0f, 1.0f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(r.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(r.y) << 23)));
+}
+
 // Two values in the 16-bit type of v.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -123,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     extern __shared__ uint8_t raw_smem[];
     AttnSmem &sm = *reinterpret_cast<AttnSmem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && blockIdx.y == 0 && a.err != nullptr)
         for (int i = threadIdx.x; i < a.n; i += kThreads) {
             int lq, lk;
@@ -151,13 +173,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             barrier_init(smem_addr(&sm.s_full[i]), 1);
-            barrier_init(smem_addr(&sm.p_full[i]), kRows);
+            barrier_init(smem_addr(&sm.p_full[i][0]), kRows);
+            barrier_init(smem_addr(&sm.p_full[i][1]), kRows);
             barrier_init(smem_addr(&sm.o_full[i]), 1);
         }
         fence_barrier_init();
     }
     __syncthreads();
-    const int q_row0 = sm.item[0], lq = sm.item[1], k_row0 = sm.item[2], lk = sm.item[3], token0 = sm.item[4];
+    const int entry = sm.item[lane & 7];
+    const auto uniform = [&](int i) { return __shfl_sync(0xffffffffu, entry, i); };
+    const int q_row0 = uniform(0), lq = uniform(1), k_row0 = uniform(2), lk = uniform(3), token0 = uniform(4);
     if (q_row0 < 0) return;
     // blockIdx.y: key head and block of `pack` query heads
     const int blocks = a.group / a.pack, kv_head = blockIdx.y / blocks, head0 = blockIdx.y * a.pack;
@@ -175,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     bool ok = true;
 
     if (warp >= 8) {
@@ -214,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t qk = tc_idesc(type, kRows, kRows, false, false) | (a.negative ? 1u << 13 : 0u);
             constexpr uint32_t pv = tc_idesc(type, kRows, kD, true);
             const auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[j % kStages]);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
@@ -230,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 for (int i = 0; i < 2; ++i)
                     if (tiles[i] > 0) scores(i, 0);
-                if (lane == 0) tc_commit(smem_addr(&sm.k_empty[0]));
+                if (elect_one()) tc_commit(smem_addr(&sm.k_empty[0]));
             }
             for (int j = 0; j < all && ok; ++j) {
                 const int s = j % kStages;
@@ -248,17 +273,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int i = 0; i < 2 && ok; ++i) {
                     if (j >= tiles[i]) continue;
-                    ok = barrier_wait(smem_addr(&sm.p_full[i]), j & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t va = smem_addr(sm.v[s]);
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = barrier_wait(smem_addr(&sm.p_full[i][half]), j & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t va = smem_addr(sm.v[s]);
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
-                        tc_commit(smem_addr(&sm.o_full[i]));
+                            for (int t = 4 * half; t < 4 * half + 4; ++t)
+                                tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
+                            if (half == 1) tc_commit(smem_addr(&sm.o_full[i]));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
                     if (j + 1 < tiles[i]) {  // the next scores go where P is: after the product that reads it
                         ok = barrier_wait(smem_addr(&sm.k_full[(j + 1) % kStages]), (j + 1) / kStages & 1) &&
                              barrier_wait(smem_addr(&sm.o_full[i]), j & 1);
@@ -267,13 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         scores(i, j + 1);
                     }
                 }
-                if (ok && lane == 0) {
+                if (ok && elect_one()) {
                     tc_commit(smem_addr(&sm.v_empty[s]));
                     if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[(j + 1) % kStages]));
                 }
                 __syncwarp();
             }
-            if (!ok && lane == 0) {  // products in flight end before the memory is given back
+            if (!ok && elect_one()) {  // products in flight end before the memory is given back
                 tc_commit(smem_addr(&sm.q_full));
                 barrier_wait(smem_addr(&sm.q_full), 1);
             }
@@ -296,33 +324,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            // the second half of the keys first, for its maximum alone; then the first half, which stays; P takes the
-            // place of the first half's columns, so the second half is still there to be read again
-            const int limit = (j + 1) * kRows > least ? sees - j * kRows : kRows;
-            uint32_t x[2][32];
-            const auto fetch = [&](int half) {
-                tmem_load32(ts + 64 * half, x[0]);
-                tmem_load32(ts + 64 * half + 32, x[1]);
-                tmem_wait_load();
-                if ((j + 1) * kRows > least) {
+            uint32_t x[4][32];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 4; ++b) tmem_load32(ts + 32 * b, x[b]);
+            tmem_wait_load();
+            const bool masked = (j + 1) * kRows > least;  // some row of the tile does not see all of these keys
+            if (masked) {
+                const int limit = sees - j * kRows;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (64 * half + 32 * b + e >= limit) x[b][e] = 0xff800000u;
-                }
-            };
-            const auto largest = [&](float m) {
+                for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * b + e >= limit) x[b][e] = 0xff800000u;
+            }
+            float ms[4];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) m = max3(m, f_of(x[b][e]), f_of(x[b][e + 1]));
-                return m;
-            };
-            fetch(1);
-            float m = largest(-INFINITY);
-            fetch(0);
-            m = largest(m) * c;
+            for (int b = 0; b < 4; ++b) {
+                ms[b] = fmaxf(f_of(x[b][0]), f_of(x[b][1]));
+#pragma unroll
+                for (int e = 2; e < 32; e += 2) ms[b] = max3(ms[b], f_of(x[b][e]), f_of(x[b][e + 1]));
+            }
+            const float m = max3(fmaxf(ms[0], ms[1]), ms[2], ms[3]) * c;
             const bool moves = m > top + 8.0f;
             if (__any_sync(0xffffffffu, moves)) {
                 const float now = moves ? m : top;
@@ -342,25 +364,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float off = top == -INFINITY ? 0.0f : -top;
-            float2 part = make_float2(0.0f, 0.0f);
+            const auto halves = [&](auto polynomial) {
+                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half == 1) fetch(1);
-                uint32_t w[32];
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const uint32_t *s = &x[e >> 4][2 * (e & 15)];
-                    float2 z = __ffma2_rn(make_float2(f_of(s[0]), f_of(s[1])), make_float2(c, c), make_float2(off, off));
-                    z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-                    part = __fadd2_rn(part, z);
-                    w[e] = pack2<BF16>(z.x, z.y);
+                    for (int e = 0; e < 32; ++e) {
+                        const uint32_t *s = &x[2 * half + (e >> 4)][2 * (e & 15)];
+                        float2 z = __ffma2_rn(make_float2(f_of(s[0]), f_of(s[1])), make_float2(c, c), make_float2(off, off));
+                        if (e % 8 < decltype(polynomial)::value) z = exp2_polynomial(z);
+                        else z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                        part[e & 1] = __fadd2_rn(part[e & 1], z);
+                        w[e] = pack2<BF16>(z.x, z.y);
+                    }
+                    tmem_store32(ts + 32 * half, w);
+                    tmem_wait_store();
+                    tc_fence_before();
+                    barrier_arrive(smem_addr(&sm.p_full[i][half]));
                 }
-                tmem_store32(ts + 32 * half, w);
-            }
-            sum += part.x + part.y;
-            tmem_wait_store();
-            tc_fence_before();
-            barrier_arrive(smem_addr(&sm.p_full[i]));
+                sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+            };
+            if (masked) halves(std::integral_constant<int, 0>());
+            else halves(std::integral_constant<int, kPolynomial>());
         }
         if (ok && tiles[i] > 0) ok = barrier_wait(smem_addr(&sm.o_full[i]), (tiles[i] - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);

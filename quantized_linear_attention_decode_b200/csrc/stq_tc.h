@@ -5,6 +5,16 @@
 
 namespace stq {
 
+// True in one lane of a converged warp.  Branching on this, and not on the lane's number, lets the
+// compiler keep what the branch computes in uniform registers, where tcgen05.mma wants its
+// descriptors (moving them there took 100 cycles a product, against 64 that it runs).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Takes `columns` (a power of two >= 32) of tensor memory; the address goes to shared memory.  One whole warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns)
 {
