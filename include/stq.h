@@ -403,6 +403,7 @@ typedef struct {
  * stq_quantize_state do it.  Decoding goes on from there with stq_decode_step.
  *   seq_start: device int32 [n + 1].  A range that is not within [0, total] or
  *              runs backwards is taken as empty and reported (STQ_ERR_INDEX).
+ *              Ranges that overlap have undefined results.
  *              An empty one leaves its page as it is, or zero if fresh.
  *   total:     tokens (rows) of the token arrays; rows of no entry are neither
  *              read into a result nor written.

@@ -640,7 +640,8 @@ stq_status stq_prompt_workspace(const stq_pool *p, int32_t n, int32_t total, siz
 {
     if (p == nullptr || bytes == nullptr) return fail(STQ_ERR_ARG, "NULL argument");
     if (n < 0 || total < 0) return fail(STQ_ERR_ARG, "n = %d, total = %d", n, total);
-    *bytes = 256;
+    // whatever the type of the rows turns out to be
+    *bytes = std::max<size_t>(256, (size_t)stq::prompt_chunks(n, total) * p->H * stq::kPreparedBytes);
     return STQ_OK;
 }
 

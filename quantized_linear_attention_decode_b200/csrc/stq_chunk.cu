@@ -1,0 +1,731 @@
+// stq_chunk.cu -- the gated delta rule over whole prompts in chunks of 64 tokens (sm_100a).
+//
+// Within a chunk that starts from the state X_0, with R_ti the product of the decays
+// behind token i up to t (R_t the product from the chunk's start, D_i = R_63,i) and
+//   u_t = b_t (v_t - a_t X_{t-1}^T k_t),   X_t = R_t X_0 + sum_{i <= t} R_ti k_i u_i^T,
+// the rows u solve a triangular system, and all that remains is products:
+//   U   = T diag(b) (V - diag(R) K X_0),   T = (I + A)^-1,  A_ti = b_t R_ti k_t.k_i  (i < t)
+//   Y   = diag(R) Q X_0 + P U,             P_ti = R_ti q_t.k_i                        (i <= t)
+//   X_C = R_63 X_0 + K^T diag(D) U.
+// T and P do not depend on the state: prepare_kernel computes them for all chunks and
+// heads at once.  chunk_kernel then walks over a prompt's chunks, one CTA a head.
+//
+// Precision.  The state has to come out as the recurrence in fp32 gives it.  k is a
+// 16-bit value, exact in tf32 (11 bits); X_0, V - K X_0, T and D U are fp32 values
+// and enter the tensor core as two tf32 terms, x = hi + lo with hi rounded to
+// nearest, 2^-21 of x left: 2 products against k, 3 of the 4 for T times a vector.  Y
+// is rounded to 16 bits and takes one term of each (2^-11).  Sums are fp32.
+#include <cmath>
+
+#include "stq_host.h"
+#include "stq_tc.h"
+
+namespace stq {
+namespace {
+
+constexpr int kC = kPromptChunk;  // tokens of a chunk
+
+// What prepare_kernel leaves for one (chunk, head): T diag(b) and P, the ten 16 x 16 blocks on and
+// below the diagonal each (block (i, j) at i (i + 1) / 2 + j), then R_t and D_t.
+constexpr int kBlockFloats = 256, kTriangle = 10 * kBlockFloats;
+struct Prepared {
+    float t[kTriangle], p[kTriangle], r[kC], d[kC];
+};
+static_assert(sizeof(Prepared) == kPreparedBytes, "workspace size");
+
+// Where chunk `at` of entry e has its Prepared: distinct for ranges that do not overlap, and within
+// prompt_chunks(n, total) for any range within [0, total].
+__device__ __forceinline__ Prepared *prepared(const PromptIO &io, int H, int e, int at, int h)
+{
+    const long long chunk = io.span.seq_start[e] / kC + e + at;
+    return reinterpret_cast<Prepared *>(io.workspace) + chunk * H + h;
+}
+
+__device__ __forceinline__ int block_of(int i, int j) { return (i * (i + 1) / 2 + j) * kBlockFloats; }
+
+// x rounded to tf32, to nearest; what is left of it.
+__device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
+
+// ---------------------------------------------------------------- T and P of every chunk
+
+constexpr int kPrepThreads = 128;
+constexpr int kPrepRow = kD + 8;  // 16-bit values of a row in shared memory: eight rows on eight different banks
+
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+struct PrepSmem {
+    union {
+        struct {
+            uint16_t k[kC][kPrepRow], q[kC][kPrepRow];
+        } in;
+        struct {
+            float a[kC][kC + 4], t[kC][kC + 4];
+        } m;
+    };
+    float r[kC][kC + 1];
+    float w[3][16][20];
+    float alpha[kC], beta[kC];
+    int item[3];
+};
+
+// The entry and the chunk of it that `chunk` of all is; the whole warp calls it.  False: there are not so many.
+__device__ __forceinline__ bool find_chunk(const PromptIO &io, int chunk, int *entry, int *at)
+{
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int first = 0; first < io.n; first += 32) {
+        const int len = first + lane < io.n ? io.span.length(first + lane) : 0;
+        const int mine = len > 0 ? (len + kC - 1) / kC : 0;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, base + upto > chunk);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            *entry = first + who;
+            *at = chunk - base - __shfl_sync(0xffffffffu, upto - mine, who);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+// Bound by the tensor products (2 x 64 x 64 x 128 of 16-bit values) no more than by the
+// inverse: its diagonal blocks of 16 by substitution, a thread a column, the others
+// by block products in fp32.  Four CTAs on an SM hide each other's latencies.
+template <bool BF16>
+__global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, int H)
+{
+    extern __shared__ __align__(16) uint8_t raw_smem[];
+    PrepSmem &s = *reinterpret_cast<PrepSmem *>(raw_smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int h = blockIdx.y;
+    if (warp == 0) {
+        int e = 0, at = 0;
+        const bool found = find_chunk(io, blockIdx.x, &e, &at);
+        if (lane == 0) {
+            s.item[0] = found ? e : -1;
+            s.item[1] = at;
+        }
+    }
+    __syncthreads();
+    const int e = s.item[0];
+    if (e < 0) return;
+    const long long row0 = io.span.seq_start[e] + static_cast<long long>(s.item[1]) * kC;
+    const int m = min(kC, io.span.length(e) - s.item[1] * kC);
+    Prepared *out = prepared(io, H, e, s.item[1], h);
+    for (int i = tid; i < kC * kD / 8; i += kPrepThreads) {
+        const int t = i / (kD / 8), d = i % (kD / 8) * 8;
+        uint4 kk = make_uint4(0, 0, 0, 0), qq = kk;
+        if (t < m) {
+            kk = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(io.k.data) + (row0 + t) * io.k.token_stride + h * io.k.head_stride + d);
+            qq = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(io.q.data) + (row0 + t) * io.q.token_stride + h * io.q.head_stride + d);
+        }
+        *reinterpret_cast<uint4 *>(&s.in.k[t][d]) = kk;
+        *reinterpret_cast<uint4 *>(&s.in.q[t][d]) = qq;
+    }
+    if (tid < kC) {
+        s.alpha[tid] = tid < m ? io.alpha[(row0 + tid) * H + h] : 1.0f;
+        s.beta[tid] = tid < m ? io.beta[(row0 + tid) * H + h] : 0.0f;
+    }
+    __syncthreads();
+    // R by running products (no logarithms: a decay may be zero or negative)
+    if (tid < kC) {
+        float r = 1.0f;
+        for (int t = tid; t < kC; ++t) {
+            if (t > tid) r *= s.alpha[t];
+            s.r[t][tid] = r;
+        }
+        out->d[tid] = r;
+    } else if (tid == kC) {
+        float r = 1.0f;
+        for (int t = 0; t < kC; ++t) out->r[t] = r *= s.alpha[t];
+    }
+    // k k^T and q k^T, rows 16 warp .. + 15, columns up to the diagonal
+    float kk[8][4], qk[8][4];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kk[nt][j] = qk[nt][j] = 0.0f;
+    const uint32_t k0 = smem_addr(&s.in.k[0][0]), q0 = smem_addr(&s.in.q[0][0]);
+    const uint32_t arow = (16 * warp + (lane & 15)) * (kPrepRow * 2) + (lane >> 4) * 16;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        uint32_t ka[4], qa[4];
+        load_matrices(ka, k0 + arow + ks * 32);
+        load_matrices(qa, q0 + arow + ks * 32);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            if (np > warp) continue;
+            uint32_t b[4];  // rows 16 np .. + 7 and + 8 .. + 15, both halves of the step
+            load_matrices(b, k0 + (16 * np + (lane & 7) + (lane >> 4) * 8) * (kPrepRow * 2) + ks * 32 + (lane >> 3 & 1) * 16);
+            mma16<BF16>(kk[2 * np], ka, b[0], b[1]);
+            mma16<BF16>(kk[2 * np + 1], ka, b[2], b[3]);
+            mma16<BF16>(qk[2 * np], qa, b[0], b[1]);
+            mma16<BF16>(qk[2 * np + 1], qa, b[2], b[3]);
+        }
+    }
+    __syncthreads();  // k and q are read, R is there
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        if (nt / 2 > warp) continue;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 16 * warp + g + 8 * half, i = 8 * nt + 2 * t4;
+            float a[2], p[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float r = i + j <= t ? s.r[t][i + j] : 0.0f;
+                a[j] = i + j < t ? s.beta[t] * (r * kk[nt][2 * half + j]) : 0.0f;
+                p[j] = i + j <= t ? tf32_hi(r * qk[nt][2 * half + j]) : 0.0f;
+            }
+            *reinterpret_cast<float2 *>(&s.m.a[t][i]) = make_float2(a[0], a[1]);
+            *reinterpret_cast<float2 *>(out->p + block_of(warp, nt / 2) + (t & 15) * 16 + (i & 15)) = make_float2(p[0], p[1]);
+        }
+    }
+    __syncthreads();
+    // the inverses of the diagonal blocks
+    if (tid < kC) {
+        const int b = tid >> 4, c = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float y = i == c ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) y = fmaf(-s.m.a[16 * b + i][16 * b + j], x[j], y);
+            x[i] = y;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s.m.t[16 * b + i][16 * b + c] = x[i];
+    }
+    __syncthreads();
+    // T_ij = -T_ii sum_{j <= k < i} A_ik T_kj, by distance from the diagonal
+    const int r = tid >> 3, c = (tid & 7) * 2;
+    for (int dist = 1; dist < 4; ++dist) {
+        for (int j = 0; j + dist < 4; ++j) {
+            const int i = j + dist;
+            float2 w = make_float2(0.0f, 0.0f);
+            for (int k = 16 * j; k < 16 * i; ++k) {
+                const float a = s.m.a[16 * i + r][k];
+                const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[k][16 * j + c]);
+                w = make_float2(fmaf(a, y.x, w.x), fmaf(a, y.y, w.y));
+            }
+            *reinterpret_cast<float2 *>(&s.w[j][r][c]) = w;
+        }
+        __syncthreads();
+        for (int j = 0; j + dist < 4; ++j) {
+            const int i = j + dist;
+            float2 w = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float a = -s.m.t[16 * i + r][16 * i + k];
+                const float2 y = *reinterpret_cast<const float2 *>(&s.w[j][k][c]);
+                w = make_float2(fmaf(a, y.x, w.x), fmaf(a, y.y, w.y));
+            }
+            *reinterpret_cast<float2 *>(&s.m.t[16 * i + r][16 * j + c]) = w;
+        }
+        __syncthreads();
+    }
+    for (int x = tid; x < kTriangle / 2; x += kPrepThreads) {
+        const int blk = x / (kBlockFloats / 2), in = x % (kBlockFloats / 2) * 2;
+        int i = 0;
+        while ((i + 1) * (i + 2) / 2 <= blk) ++i;
+        const int j = blk - i * (i + 1) / 2, t = 16 * i + in / 16, col = 16 * j + in % 16;
+        const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[t][col]);
+        *reinterpret_cast<float2 *>(out->t + 2 * x) = make_float2(y.x * s.beta[col], y.y * s.beta[col + 1]);
+    }
+}
+
+// ---------------------------------------------------------------- the walk over the chunks
+//
+// Transposed throughout: lane j of tensor memory is column j of the state (and of V, U
+// and Y), so X_0^T, (V - K X_0)^T, U^T are the products' A operands straight from
+// tensor memory, and what threads do between the products is their own row's.  B operands
+// (K, Q, K^T, T, P, as fp32 in 128-byte swizzled rows) are written to shared memory by four
+// warps that run ahead.  Columns of tensor memory:
+//     0  X^T, the sum that the chunk's update goes onto, scaled by R_63 beforehand
+//   128  X_0^T hi; after the products with K and Q: (D U)^T hi | lo
+//   256  X_0^T lo; after the product with K: (V - R K X_0)^T hi | lo; after T: U^T hi
+//   384  (K X_0)^T; then U^T
+//   448  (diag(R) Q X_0)^T, then Y^T
+// Bound by the chain of a chunk's products and what stands between them: 3200 cycles
+// of products, of which all but Y's are in a row.
+
+constexpr int kGroupThreads = 256;  // warps 0-7: two for each quarter of the lanes, half of the columns each
+constexpr int kFeedThreads = 128;   // warps 8-11
+constexpr int kChunkThreads = kGroupThreads + kFeedThreads + 32;
+constexpr uint32_t kColX = 0, kColHi = 128, kColLo = 256, kColK = 384, kColY = 448;
+
+struct __align__(1024) ChunkSmem {
+    uint8_t k[kC * kD * 4], q[kC * kD * 4];   // 4 blocks of 32 dims: 64 rows of 128 bytes
+    uint8_t kt[kC * kD * 4];                  // 2 blocks of 32 tokens: 128 rows
+    uint8_t t_hi[kC * kC * 4], t_lo[kC * kC * 4], p[kC * kC * 4];  // 2 blocks of 32 tokens: 64 rows
+    uint16_t v[2][kC][kD];
+    float r[2][kC], d[2][kC];
+    unsigned long long kq_full, kq_empty, kt_full, kt_empty, tp_full, tp_empty, v_full[2], v_empty[2];
+    unsigned long long x_full, k_done, r_full, u_done, u_full, y_done, y_empty, x_done;
+    uint32_t tmem;
+    int item[4];
+};
+
+__device__ __forceinline__ void tc_mma_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// Byte of element (row, col) of a B operand with `rows` rows: blocks of 32 columns, 16-byte pieces exchanged by row.
+__device__ __forceinline__ uint32_t swizzled(int rows, int row, int col)
+{
+    return static_cast<uint32_t>((col >> 5) * rows * 128 + row * 128 + (((col >> 2 & 7) ^ (row & 7)) << 4) + (col & 3) * 4);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t w)
+{
+    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float widen1(uint16_t w)
+{
+    if (BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
+    return __half2float(*reinterpret_cast<const __half *>(&w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t narrow1(float x)
+{
+    if (BF16) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(x);
+        return *reinterpret_cast<const uint16_t *>(&h);
+    }
+    const __half h = __float2half_rn(x);
+    return *reinterpret_cast<const uint16_t *>(&h);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, PromptIO io)
+{
+    extern __shared__ uint8_t raw_smem[];
+    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int H = pool.H, h = blockIdx.x % H;
+    // long prompts first: the entry of this rank by length (all CTAs agree on the order); in their order where
+    // there are too many to rank
+    if (io.n <= kFeedThreads) {
+        if (tid < io.n) {
+            const int len = io.span.length(tid);
+            int rank = 0;
+            for (int i = 0; i < io.n; ++i) {
+                const int other = io.span.length(i);
+                rank += other > len || (other == len && i < tid);
+            }
+            if (rank == static_cast<int>(blockIdx.x) / H) sm.item[0] = tid;
+        }
+    } else if (tid == 0) {
+        sm.item[0] = blockIdx.x / H;
+    }
+    __syncthreads();
+    const int e = __shfl_sync(0xffffffffu, sm.item[0], 0);
+    const int req = io.req_idx[e], slot = io.slot_idx[e];
+    if (req < 0 || req >= pool.R || slot < 0 || slot >= pool.S) {
+        if (tid == 0) atomicOr(pool.err, kErrIndex);
+        return;
+    }
+    int len = io.span.length(e);
+    if (len < 0) {
+        if (tid == 0) atomicOr(pool.err, kErrIndex);
+        len = 0;
+    }
+    const bool fresh = io.span.is_fresh(e);
+    float *state = io.state + (static_cast<size_t>(e) * H + h) * kD * kD;
+    if (len == 0) {
+        if (fresh)
+            for (int i = tid; i < kD * kD / 4; i += kChunkThreads) reinterpret_cast<float4 *>(state)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        return;
+    }
+    const int chunks = (len + kC - 1) / kC;
+    const long long first = io.span.seq_start[e];
+    if (warp == 12) {
+        if (lane == 0) {
+            const auto init = [](unsigned long long &b, uint32_t count) { barrier_init(smem_addr(&b), count); };
+            init(sm.kq_full, kFeedThreads);
+            init(sm.kq_empty, 1);
+            init(sm.kt_full, kFeedThreads);
+            init(sm.kt_empty, 1);
+            init(sm.tp_full, kFeedThreads);
+            init(sm.tp_empty, 1);
+            for (int i = 0; i < 2; ++i) {
+                init(sm.v_full[i], kFeedThreads);
+                init(sm.v_empty[i], kGroupThreads);
+            }
+            init(sm.x_full, kGroupThreads);
+            init(sm.k_done, 1);
+            init(sm.r_full, kGroupThreads);
+            init(sm.u_done, 1);
+            init(sm.u_full, kGroupThreads);
+            init(sm.y_done, 1);
+            init(sm.y_empty, kGroupThreads);
+            init(sm.x_done, 1);
+            fence_barrier_init();
+        }
+        __syncwarp();
+        tmem_alloc(smem_addr(&sm.tmem), 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+    const Prepared *prep = prepared(io, H, e, 0, h);
+    bool ok = true;
+
+    if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------ B operands, V, R and D of the chunks
+        const int ft = tid - kGroupThreads, fw = warp - 8;
+        for (int i = ft; i < kC * kC / 4; i += kFeedThreads) {  // above the diagonal they stay zero
+            reinterpret_cast<uint4 *>(sm.t_hi)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.t_lo)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        for (int c = 0; c < chunks && ok; ++c, prep += H) {
+            const long long row0 = first + static_cast<long long>(c) * kC;
+            const int m = min(kC, len - c * kC);
+            // V, R and D: two buffers
+            const int vb = c & 1;
+            if (c >= 2) ok = barrier_wait(smem_addr(&sm.v_empty[vb]), (c >> 1 & 1) ^ 1);
+            if (!ok) break;
+            for (int i = ft; i < kC * kD / 8; i += kFeedThreads) {
+                const int t = i / (kD / 8), d = i % (kD / 8) * 8;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (t < m) x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(io.v.data) + (row0 + t) * io.v.token_stride + h * io.v.head_stride + d);
+                *reinterpret_cast<uint4 *>(&sm.v[vb][t][d]) = x;
+            }
+            if (ft < kC) sm.r[vb][ft] = prep->r[ft];
+            else sm.d[vb][ft - kC] = prep->d[ft - kC];
+            barrier_arrive(smem_addr(&sm.v_full[vb]));
+            // a lane's two tokens, 32 dims of k and q each
+            uint32_t kw[2][16], qw[2][16];
+            float rt[2];
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                const int t = 32 * pass + lane;
+                rt[pass] = prep->r[t];
+                const uint16_t *kp = static_cast<const uint16_t *>(io.k.data) + (row0 + t) * io.k.token_stride + h * io.k.head_stride + 32 * fw;
+                const uint16_t *qp = static_cast<const uint16_t *>(io.q.data) + (row0 + t) * io.q.token_stride + h * io.q.head_stride + 32 * fw;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    if (t < m) {
+                        x = *reinterpret_cast<const uint4 *>(kp + 8 * i);
+                        y = *reinterpret_cast<const uint4 *>(qp + 8 * i);
+                    }
+                    kw[pass][4 * i] = x.x; kw[pass][4 * i + 1] = x.y; kw[pass][4 * i + 2] = x.z; kw[pass][4 * i + 3] = x.w;
+                    qw[pass][4 * i] = y.x; qw[pass][4 * i + 1] = y.y; qw[pass][4 * i + 2] = y.z; qw[pass][4 * i + 3] = y.w;
+                }
+            }
+            if (c > 0) ok = barrier_wait(smem_addr(&sm.kq_empty), (c & 1) ^ 1);
+            if (!ok) break;
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                const int t = 32 * pass + lane;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t at = swizzled(kC, t, 32 * fw + 4 * i);
+                    const float2 a = widen<BF16>(kw[pass][2 * i]), b = widen<BF16>(kw[pass][2 * i + 1]);
+                    *reinterpret_cast<float4 *>(sm.k + at) = make_float4(a.x, a.y, b.x, b.y);
+                    const float2 x = widen<BF16>(qw[pass][2 * i]), y = widen<BF16>(qw[pass][2 * i + 1]);
+                    *reinterpret_cast<float4 *>(sm.q + at) =
+                        make_float4(tf32_hi(x.x * rt[pass]), tf32_hi(x.y * rt[pass]), tf32_hi(y.x * rt[pass]), tf32_hi(y.y * rt[pass]));
+                }
+            }
+            fence_async_smem();
+            barrier_arrive(smem_addr(&sm.kq_full));
+            // T and P: ten blocks each, 16 threads a block row... 5 vectors a thread of each
+            float4 tv[5], pv[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                tv[i] = *reinterpret_cast<const float4 *>(prep->t + 4 * (ft + kFeedThreads * i));
+                pv[i] = *reinterpret_cast<const float4 *>(prep->p + 4 * (ft + kFeedThreads * i));
+            }
+            if (c > 0) ok = barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int x = ft + kFeedThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
+                const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
+                const uint32_t at = swizzled(kC, 16 * bi + in / 16, 16 * bj + in % 16);
+                const float4 hi = make_float4(tf32_hi(tv[i].x), tf32_hi(tv[i].y), tf32_hi(tv[i].z), tf32_hi(tv[i].w));
+                *reinterpret_cast<float4 *>(sm.t_hi + at) = hi;
+                *reinterpret_cast<float4 *>(sm.t_lo + at) = make_float4(tv[i].x - hi.x, tv[i].y - hi.y, tv[i].z - hi.z, tv[i].w - hi.w);
+                *reinterpret_cast<float4 *>(sm.p + at) = pv[i];
+            }
+            fence_async_smem();
+            barrier_arrive(smem_addr(&sm.tp_full));
+            if (c > 0) ok = barrier_wait(smem_addr(&sm.kt_empty), (c & 1) ^ 1);
+            if (!ok) break;
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                const int t = 32 * pass + lane;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 a = widen<BF16>(kw[pass][i]);
+                    *reinterpret_cast<float *>(sm.kt + swizzled(kD, 32 * fw + 2 * i, t)) = a.x;
+                    *reinterpret_cast<float *>(sm.kt + swizzled(kD, 32 * fw + 2 * i + 1, t)) = a.y;
+                }
+            }
+            fence_async_smem();
+            barrier_arrive(smem_addr(&sm.kt_full));
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------ products
+        constexpr uint32_t n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
+        const uint32_t k = smem_addr(sm.k), q = smem_addr(sm.q), kt = smem_addr(sm.kt);
+        const uint32_t th = smem_addr(sm.t_hi), tl = smem_addr(sm.t_lo), p = smem_addr(sm.p);
+        for (int c = 0; c < chunks && ok; ++c) {
+            const uint32_t phase = c & 1;
+            ok = barrier_wait(smem_addr(&sm.kq_full), phase) && barrier_wait(smem_addr(&sm.x_full), phase);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                    for (int s = 0; s < 16; ++s)
+                        tc_mma_tf32(tmem + kColK, tmem + (term ? kColLo : kColHi) + 8 * s, tc_desc(k + (s >> 2) * 8192 + (s & 3) * 32, 16, 1024), n64, term > 0 || s > 0);
+                tc_commit(smem_addr(&sm.k_done));
+            }
+            __syncwarp();
+            if (c > 0) ok = barrier_wait(smem_addr(&sm.y_empty), phase ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 16; ++s)
+                    tc_mma_tf32(tmem + kColY, tmem + kColHi + 8 * s, tc_desc(q + (s >> 2) * 8192 + (s & 3) * 32, 16, 1024), n64, s > 0);
+                tc_commit(smem_addr(&sm.kq_empty));
+            }
+            __syncwarp();
+            ok = barrier_wait(smem_addr(&sm.tp_full), phase) && barrier_wait(smem_addr(&sm.r_full), phase);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                // rows of T from the step's own block of 16 on: those before it have zeros there
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const int b = s >> 1;
+                        tc_mma_tf32(tmem + kColK + 16 * b, tmem + kColLo + (term == 2 ? 64 : 0) + 8 * s,
+                                    tc_desc((term == 1 ? tl : th) + (s >> 2) * 8192 + (s & 3) * 32 + b * 2048, 16, 1024),
+                                    tc_idesc(2, 128, 64 - 16 * b, false), term > 0 || s > 0);
+                    }
+                tc_commit(smem_addr(&sm.u_done));
+            }
+            __syncwarp();
+            ok = barrier_wait(smem_addr(&sm.kt_full), phase) && barrier_wait(smem_addr(&sm.u_full), phase);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const int b = s >> 1;
+                    tc_mma_tf32(tmem + kColY + 16 * b, tmem + kColLo + 8 * s, tc_desc(p + (s >> 2) * 8192 + (s & 3) * 32 + b * 2048, 16, 1024),
+                                tc_idesc(2, 128, 64 - 16 * b, false), true);
+                }
+                tc_commit(smem_addr(&sm.y_done));
+                tc_commit(smem_addr(&sm.tp_empty));
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        tc_mma_tf32(tmem + kColX, tmem + kColHi + 64 * term + 8 * s, tc_desc(kt + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024), n128, true);
+                tc_commit(smem_addr(&sm.x_done));
+                tc_commit(smem_addr(&sm.kt_empty));
+            }
+            __syncwarp();
+        }
+        if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
+            barrier_init(smem_addr(&sm.item), 1);
+            tc_commit(smem_addr(&sm.item));
+            barrier_wait(smem_addr(&sm.item), 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ between the products: a lane is a column of the state
+        const int half = warp >> 2, j = (warp & 3) * 32 + lane;
+        const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        // X_0 and its terms, 32 key rows at a time; x_next: R_63 of the chunk that starts
+        const auto put = [&](int col, uint32_t (&x)[32], float x_next) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
+            tmem_store32(base + kColHi + col, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
+            tmem_store32(base + kColLo + col, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) * x_next);
+            tmem_store32(base + kColX + col, w);
+        };
+        ok = barrier_wait(smem_addr(&sm.v_full[0]), 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            const float x_next = sm.r[0][kC - 1];
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int col = 64 * half + 32 * b;
+                uint32_t x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = fresh ? 0u : __float_as_uint(state[static_cast<size_t>(col + i) * kD + j]);
+                put(col, x, x_next);
+            }
+            tmem_wait_store();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.x_full));
+        }
+        for (int c = 0; c < chunks && ok; ++c) {
+            const uint32_t phase = c & 1;
+            const int vb = c & 1;
+            // V - diag(R) K X_0
+            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.k_done), phase));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[32], w[32];
+            tmem_load32(base + kColK + 32 * half, x);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int t = 32 * half + i;
+                const float v = fmaf(-sm.r[vb][t], __uint_as_float(x[i]), widen1<BF16>(sm.v[vb][t][j]));
+                x[i] = __float_as_uint(v);
+                w[i] = __float_as_uint(tf32_hi(v));
+            }
+            tmem_store32(base + kColLo + 32 * half, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
+            tmem_store32(base + kColLo + 64 + 32 * half, w);
+            tmem_wait_store();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.r_full));
+            // U, and D U
+            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.u_done), phase));
+            if (!ok) break;
+            tc_fence_after();
+            tmem_load32(base + kColK + 32 * half, x);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
+            tmem_store32(base + kColLo + 32 * half, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float u = sm.d[vb][32 * half + i] * __uint_as_float(x[i]);
+                x[i] = __float_as_uint(u);
+                w[i] = __float_as_uint(tf32_hi(u));
+            }
+            tmem_store32(base + kColHi + 32 * half, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
+            tmem_store32(base + kColHi + 64 + 32 * half, w);
+            tmem_wait_store();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.u_full));
+            barrier_arrive(smem_addr(&sm.v_empty[vb]));
+            // the state after the chunk
+            float x_next = 0.0f;
+            if (c + 1 < chunks) {
+                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.v_full[vb ^ 1]), (c + 1) >> 1 & 1));
+                if (!ok) break;
+                x_next = sm.r[vb ^ 1][kC - 1];
+            }
+            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.x_done), phase));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int col = 64 * half + 32 * b;
+                tmem_load32(base + kColX + col, x);
+                tmem_wait_load();
+                if (c + 1 < chunks) {
+                    put(col, x, x_next);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) state[static_cast<size_t>(col + i) * kD + j] = __uint_as_float(x[i]);
+                }
+            }
+            tmem_wait_store();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.x_full));
+            // Y, while the next chunk's first products run
+            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.y_done), phase));
+            if (!ok) break;
+            tc_fence_after();
+            tmem_load32(base + kColY + 32 * half, x);
+            tmem_wait_load();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.y_empty));
+            const int m = min(kC, len - c * kC) - 32 * half;
+            uint16_t *y = static_cast<uint16_t *>(io.y) + ((first + static_cast<long long>(c) * kC + 32 * half) * H + h) * kD + j;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < m) y[static_cast<size_t>(i) * H * kD] = narrow1<BF16>(__uint_as_float(x[i]));
+        }
+    }
+    if (!ok && lane == 0) atomicOr(pool.err, kErrTimeout);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+template <bool BF16>
+cudaError_t launch(const PoolView &p, const PromptIO &io, cudaStream_t stream)
+{
+    const int prep = static_cast<int>(sizeof(PrepSmem)), smem = static_cast<int>(sizeof(ChunkSmem)) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(prepare_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    prepare_kernel<BF16><<<dim3(static_cast<unsigned>(prompt_chunks(io.n, io.span.total)), static_cast<unsigned>(p.H)), kPrepThreads, prep, stream>>>(io, p.H);
+    count_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    chunk_kernel<BF16><<<static_cast<unsigned>(io.n) * p.H, kChunkThreads, smem, stream>>>(p, io);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_chunks(const PoolView &p, const PromptIO &io, cudaStream_t stream)
+{
+    return io.dtype == STQ_BF16 ? launch<true>(p, io, stream) : launch<false>(p, io, stream);
+}
+
+}  // namespace stq

@@ -21,19 +21,22 @@ def _f64(t):
 
 
 def recurrence(q, k, v, beta, alpha, X):
-    """One prompt: q, k, v [T, H, 128], beta, alpha [T, H], X [H, 128, 128] -> (y, X_T, size), all fp64; size[t] bounds
-    |q_t|^T |X| over the state's last 64 values, what y's rounded products are made of."""
+    """One prompt: q, k, v [T, H, 128], beta, alpha [T, H], X [H, 128, 128] -> (y, X_T, size), all fp64.  In chunks of 64
+    tokens y_t = R_t X_0^T q_t + sum_i R_ti (q_t . k_i) u_i with the products R of the decays; size[t] is the sum of the
+    sizes of these terms, which may cancel (one key for all tokens)."""
     X = X.copy()
-    y, size, past = np.zeros_like(q), np.zeros_like(q), [np.abs(X)]
+    y, size = np.zeros_like(q), np.zeros_like(q)
     for t in range(len(q)):
+        if t % 64 == 0:
+            start, r0, r, us = np.abs(X), np.ones(q.shape[1]), np.zeros((0, q.shape[1])), np.zeros((0, *q.shape[1:]))
         X = alpha[t][:, None, None] * X
         u = beta[t][:, None] * (v[t] - np.einsum("hi,hij->hj", k[t], X))
         X = X + k[t][:, :, None] * u[:, None, :]
         y[t] = np.einsum("hi,hij->hj", q[t], X)
-        past = past[-63:] + [np.abs(X)]
-        if t % 16 == 0 or t == len(q) - 1:
-            top = np.max(past, 0)
-        size[t] = np.einsum("hi,hij->hj", np.abs(q[t]), np.maximum(top, np.abs(X)))
+        r0, r = r0 * np.abs(alpha[t]), np.concatenate([r * np.abs(alpha[t]), np.ones((1, q.shape[1]))])
+        us = np.concatenate([us, np.abs(u)[None]])
+        p = r * np.abs(np.einsum("hi,thi->th", q[t], k[t - t % 64:t + 1]))
+        size[t] = r0[:, None] * np.einsum("hi,hij->hj", np.abs(q[t]), start) + np.einsum("th,thj->hj", p, us)
     return y, X, size
 
 
@@ -77,7 +80,7 @@ class _Prompts:
 
     def check(self):
         """fp32: 1e-5 of the head's largest value, the tolerance of the decode step.  A 16-bit y is rounded once (half a
-        step of itself) and its products may be rounded to 11 bits: 2^-11 of every term, two roundings."""
+        step of itself) and the two factors of every product of its chunk's form to 11 bits: 2 times 2^-11 of every term."""
         half = torch.finfo(self.dt).eps / 2
         y, state = _f64(self.y), _f64(self.state)
         for e, m in enumerate(self.lens):
