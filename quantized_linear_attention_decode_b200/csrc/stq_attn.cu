@@ -32,9 +32,8 @@
 #include <algorithm>
 #include <cmath>
 
-#include <cuda.h>
-
 #include "stq_host.h"
+#include "stq_map.h"
 #include "stq_tc.h"
 
 namespace stq {
@@ -403,47 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// cuTensorMapEncodeTiled, from the driver that the runtime has loaded.
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled()
-{
-    static const EncodeTiled f = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
-// Rows [tokens][heads][128] in boxes of 64 dims x `box_heads` heads x `box_tokens` tokens.
-bool make_map(CUtensorMap *map, const stq_rows *r, int32_t dtype, int tokens, int heads, int box_heads, int box_tokens)
-{
-    const EncodeTiled encode = encode_tiled();
-    if (encode == nullptr) return false;
-    // a dimension of one element has no stride; the map wants some valid one
-    const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? r->head_stride : kD) * 2,
-                                   static_cast<cuuint64_t>(tokens > 1 ? r->token_stride : kD) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
-    const cuuint32_t step[3] = {1, 1, 1};
-    return encode(map, dtype == STQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                  const_cast<void *>(r->data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 stq_status check_rows(const stq_rows *r, const char *name, int32_t dtype, int32_t heads, int32_t tokens)
 {
     if (r == nullptr) return fail_status(STQ_ERR_ARG, "%s is NULL", name);
     if (tokens > 0 && r->data == nullptr) return fail_status(STQ_ERR_ARG, "%s.data is NULL", name);
     if (!rows_aligned(r, dtype)) return fail_status(STQ_ERR_ARG, "%s: rows must start on 16-byte boundaries", name);
-    const int64_t most = int64_t(1) << 38;
-    if ((heads > 1 && (r->head_stride <= 0 || r->head_stride >= most)) || (tokens > 1 && (r->token_stride <= 0 || r->token_stride >= most)))
+    if (!rows_mappable(*r, heads, tokens))
         return fail_status(STQ_ERR_UNSUPPORTED, "%s: strides must be positive (and below 2^38)", name);
     return STQ_OK;
 }
@@ -489,8 +453,8 @@ extern "C" stq_status stq_attn_prompt(const int32_t *q_start, const int32_t *k_s
     // without any key the maps of k and v are not used: q's stand in
     const stq_rows *kr = total_k > 0 ? k : q, *vr = total_k > 0 ? v : q;
     const int kt = total_k > 0 ? total_k : total_q, kh = total_k > 0 ? num_kv_heads : num_heads;
-    if (!stq::make_map(&qm, q, dtype, total_q, num_heads, pack, stq::kRows / pack) ||
-        !stq::make_map(&km, kr, dtype, kt, kh, 1, stq::kRows) || !stq::make_map(&vm, vr, dtype, kt, kh, 1, stq::kRows))
+    if (!stq::make_map(&qm, *q, dtype, total_q, num_heads, pack, stq::kRows / pack) ||
+        !stq::make_map(&km, *kr, dtype, kt, kh, 1, stq::kRows) || !stq::make_map(&vm, *vr, dtype, kt, kh, 1, stq::kRows))
         return fail_status(STQ_ERR_CUDA, "tensor map");
     stq::PromptAttn a;
     a.q_start = q_start;

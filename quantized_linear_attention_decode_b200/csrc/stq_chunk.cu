@@ -18,6 +18,7 @@
 #include <cmath>
 
 #include "stq_host.h"
+#include "stq_map.h"
 #include "stq_tc.h"
 
 namespace stq {
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, i
 // Transposed throughout: lane j of tensor memory is column j of the state (and of V, U
 // and Y), so X_0^T, (V - K X_0)^T, U^T are the products' A operands straight from
 // tensor memory, and what threads do between the products is their own row's.  B operands
-// (K, Q, K^T, T, P, as fp32 in 128-byte swizzled rows) are written to shared memory by four
+// (K, Q, K^T, T, P, as fp32 in 128-byte swizzled rows) are written to shared memory by six
 // warps that run ahead.  Columns of tensor memory:
 //     0  X^T, the sum that the chunk's update goes onto, scaled by R_63 beforehand
 //   128  X_0^T hi; after the products with K and Q: (D U)^T hi | lo
@@ -272,17 +273,21 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, i
 // of products, of which all but Y's are in a row.
 
 constexpr int kGroupThreads = 256;  // warps 0-7: two for each quarter of the lanes, half of the columns each
-constexpr int kFeedThreads = 128;   // warps 8-11
-constexpr int kChunkThreads = kGroupThreads + kFeedThreads + 32;
+constexpr int kFeedThreads = 128;   // warps 8-11; warp 12 issues the products
+constexpr int kSideThreads = 64;    // warps 13 and 14
+constexpr int kChunkThreads = kGroupThreads + kFeedThreads + 32 + kSideThreads;
 constexpr uint32_t kColX = 0, kColHi = 128, kColLo = 256, kColK = 384, kColY = 448;
 
 struct __align__(1024) ChunkSmem {
     uint8_t k[kC * kD * 4], q[kC * kD * 4];   // 4 blocks of 32 dims: 64 rows of 128 bytes
     uint8_t kt[kC * kD * 4];                  // 2 blocks of 32 tokens: 128 rows
     uint8_t t_hi[kC * kC * 4], t_lo[kC * kC * 4], p[kC * kC * 4];  // 2 blocks of 32 tokens: 64 rows
-    uint16_t v[2][kC][kD];
-    float r[2][kC], d[2][kC];
-    unsigned long long kq_full, kq_empty, kt_full, kt_empty, tp_full, tp_empty, v_full[2], v_empty[2];
+    uint8_t raw_k[2][kC * 128], raw_q[2][kC * 128], v[2][kC * 128];  // as they come: 64 dims, 128-byte swizzled rows
+    float tp_raw[2 * kTriangle];
+    struct {
+        float r[kC], d[kC];
+    } rd[2];
+    unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, tp_full, tp_empty, v_full, v_empty;
     unsigned long long x_full, k_done, r_full, u_done, u_full, y_done, y_empty, x_done;
     uint32_t tmem;
     int item[4];
@@ -329,7 +334,8 @@ __device__ __forceinline__ uint16_t narrow1(float x)
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, PromptIO io)
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                                                              const __grid_constant__ CUtensorMap v_map, PoolView pool, PromptIO io)
 {
     extern __shared__ uint8_t raw_smem[];
     ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -378,12 +384,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
             init(sm.kq_empty, 1);
             init(sm.kt_full, kFeedThreads);
             init(sm.kt_empty, 1);
-            init(sm.tp_full, kFeedThreads);
+            init(sm.tp_full, kSideThreads);
             init(sm.tp_empty, 1);
-            for (int i = 0; i < 2; ++i) {
-                init(sm.v_full[i], kFeedThreads);
-                init(sm.v_empty[i], kGroupThreads);
-            }
+            init(sm.kq_raw, 1);
+            init(sm.tp_raw_full, 1);
+            init(sm.v_full, 1);
+            init(sm.v_empty, kGroupThreads);
             init(sm.x_full, kGroupThreads);
             init(sm.k_done, 1);
             init(sm.r_full, kGroupThreads);
@@ -403,104 +409,127 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     const Prepared *prep = prepared(io, H, e, 0, h);
     bool ok = true;
+    // after a wait that gave up: loads in flight land before the memory is given back (no more than one phase each is)
+    const auto drain = [&] {
+        if (tid == kGroupThreads || tid == kGroupThreads + kFeedThreads + 32)
+            for (const auto *bar : {&sm.kq_raw, &sm.tp_raw_full, &sm.v_full}) {
+                barrier_wait(smem_addr(bar), 0);
+                barrier_wait(smem_addr(bar), 1);
+            }
+    };
 
     if (warp >= 8 && warp < 12) {
-        // ------------------------------------------------ B operands, V, R and D of the chunks
+        // ------------------------------------------------ K, Q and K^T of the chunks
         const int ft = tid - kGroupThreads, fw = warp - 8;
-        for (int i = ft; i < kC * kC / 4; i += kFeedThreads) {  // above the diagonal they stay zero
-            reinterpret_cast<uint4 *>(sm.t_hi)[i] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4 *>(sm.t_lo)[i] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        for (int c = 0; c < chunks && ok; ++c, prep += H) {
-            const long long row0 = first + static_cast<long long>(c) * kC;
-            const int m = min(kC, len - c * kC);
-            // V, R and D: two buffers
-            const int vb = c & 1;
-            if (c >= 2) ok = barrier_wait(smem_addr(&sm.v_empty[vb]), (c >> 1 & 1) ^ 1);
-            if (!ok) break;
-            for (int i = ft; i < kC * kD / 8; i += kFeedThreads) {
-                const int t = i / (kD / 8), d = i % (kD / 8) * 8;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (t < m) x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(io.v.data) + (row0 + t) * io.v.token_stride + h * io.v.head_stride + d);
-                *reinterpret_cast<uint4 *>(&sm.v[vb][t][d]) = x;
+        const auto fetch = [&](int c) {  // as they are, by one thread
+            const uint32_t bar = smem_addr(&sm.kq_raw);
+            barrier_expect(bar, 4 * kC * 128);
+            for (int half = 0; half < 2; ++half) {
+                tma_load3(smem_addr(sm.raw_k[half]), &k_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
+                tma_load3(smem_addr(sm.raw_q[half]), &q_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
             }
-            if (ft < kC) sm.r[vb][ft] = prep->r[ft];
-            else sm.d[vb][ft - kC] = prep->d[ft - kC];
-            barrier_arrive(smem_addr(&sm.v_full[vb]));
-            // a lane's two tokens, 32 dims of k and q each
-            uint32_t kw[2][16], qw[2][16];
+        };
+        if (ft == 0) fetch(0);
+        for (int c = 0; c < chunks && ok; ++c) {
+            const int m = min(kC, len - c * kC);
             float rt[2];
 #pragma unroll
+            for (int pass = 0; pass < 2; ++pass) rt[pass] = prep[static_cast<size_t>(c) * H].r[32 * pass + lane];
+            ok = barrier_wait(smem_addr(&sm.kq_raw), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.kq_empty), (c & 1) ^ 1));
+            if (!ok) break;
+            // a lane's two tokens, 32 dims of each a warp; rows behind the prompt's last are not its own
+            const uint8_t *rk = sm.raw_k[fw >> 1], *rq = sm.raw_q[fw >> 1];
+#pragma unroll
             for (int pass = 0; pass < 2; ++pass) {
                 const int t = 32 * pass + lane;
-                rt[pass] = prep->r[t];
-                const uint16_t *kp = static_cast<const uint16_t *>(io.k.data) + (row0 + t) * io.k.token_stride + h * io.k.head_stride + 32 * fw;
-                const uint16_t *qp = static_cast<const uint16_t *>(io.q.data) + (row0 + t) * io.q.token_stride + h * io.q.head_stride + 32 * fw;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (t < m) {
-                        x = *reinterpret_cast<const uint4 *>(kp + 8 * i);
-                        y = *reinterpret_cast<const uint4 *>(qp + 8 * i);
-                    }
-                    kw[pass][4 * i] = x.x; kw[pass][4 * i + 1] = x.y; kw[pass][4 * i + 2] = x.z; kw[pass][4 * i + 3] = x.w;
-                    qw[pass][4 * i] = y.x; qw[pass][4 * i + 1] = y.y; qw[pass][4 * i + 2] = y.z; qw[pass][4 * i + 3] = y.w;
-                }
-            }
-            if (c > 0) ok = barrier_wait(smem_addr(&sm.kq_empty), (c & 1) ^ 1);
-            if (!ok) break;
-#pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
-                const int t = 32 * pass + lane;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t at = swizzled(kC, t, 32 * fw + 4 * i);
-                    const float2 a = widen<BF16>(kw[pass][2 * i]), b = widen<BF16>(kw[pass][2 * i + 1]);
-                    *reinterpret_cast<float4 *>(sm.k + at) = make_float4(a.x, a.y, b.x, b.y);
-                    const float2 x = widen<BF16>(qw[pass][2 * i]), y = widen<BF16>(qw[pass][2 * i + 1]);
-                    *reinterpret_cast<float4 *>(sm.q + at) =
-                        make_float4(tf32_hi(x.x * rt[pass]), tf32_hi(x.y * rt[pass]), tf32_hi(y.x * rt[pass]), tf32_hi(y.y * rt[pass]));
+                    const int at = 128 * t + ((((fw & 1) * 4 + i) ^ (t & 7)) << 4);
+                    uint4 k = *reinterpret_cast<const uint4 *>(rk + at), q = *reinterpret_cast<const uint4 *>(rq + at);
+                    if (t >= m) k = q = make_uint4(0, 0, 0, 0);
+                    const uint32_t to0 = swizzled(kC, t, 32 * fw + 8 * i), to1 = swizzled(kC, t, 32 * fw + 8 * i + 4);
+                    const float2 k0 = widen<BF16>(k.x), k1 = widen<BF16>(k.y), k2 = widen<BF16>(k.z), k3 = widen<BF16>(k.w);
+                    *reinterpret_cast<float4 *>(sm.k + to0) = make_float4(k0.x, k0.y, k1.x, k1.y);
+                    *reinterpret_cast<float4 *>(sm.k + to1) = make_float4(k2.x, k2.y, k3.x, k3.y);
+                    const float2 q0 = widen<BF16>(q.x), q1 = widen<BF16>(q.y), q2 = widen<BF16>(q.z), q3 = widen<BF16>(q.w);
+                    const float r = rt[pass];
+                    *reinterpret_cast<float4 *>(sm.q + to0) = make_float4(tf32_hi(q0.x * r), tf32_hi(q0.y * r), tf32_hi(q1.x * r), tf32_hi(q1.y * r));
+                    *reinterpret_cast<float4 *>(sm.q + to1) = make_float4(tf32_hi(q2.x * r), tf32_hi(q2.y * r), tf32_hi(q3.x * r), tf32_hi(q3.y * r));
                 }
             }
             fence_async_smem();
             barrier_arrive(smem_addr(&sm.kq_full));
-            // T and P: ten blocks each, 16 threads a block row... 5 vectors a thread of each
-            float4 tv[5], pv[5];
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                tv[i] = *reinterpret_cast<const float4 *>(prep->t + 4 * (ft + kFeedThreads * i));
-                pv[i] = *reinterpret_cast<const float4 *>(prep->p + 4 * (ft + kFeedThreads * i));
-            }
-            if (c > 0) ok = barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1);
-            if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                const int x = ft + kFeedThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
-                const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
-                const uint32_t at = swizzled(kC, 16 * bi + in / 16, 16 * bj + in % 16);
-                const float4 hi = make_float4(tf32_hi(tv[i].x), tf32_hi(tv[i].y), tf32_hi(tv[i].z), tf32_hi(tv[i].w));
-                *reinterpret_cast<float4 *>(sm.t_hi + at) = hi;
-                *reinterpret_cast<float4 *>(sm.t_lo + at) = make_float4(tv[i].x - hi.x, tv[i].y - hi.y, tv[i].z - hi.z, tv[i].w - hi.w);
-                *reinterpret_cast<float4 *>(sm.p + at) = pv[i];
-            }
-            fence_async_smem();
-            barrier_arrive(smem_addr(&sm.tp_full));
+            // K^T from the same
             if (c > 0) ok = barrier_wait(smem_addr(&sm.kt_empty), (c & 1) ^ 1);
             if (!ok) break;
 #pragma unroll
             for (int pass = 0; pass < 2; ++pass) {
                 const int t = 32 * pass + lane;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 a = widen<BF16>(kw[pass][i]);
-                    *reinterpret_cast<float *>(sm.kt + swizzled(kD, 32 * fw + 2 * i, t)) = a.x;
-                    *reinterpret_cast<float *>(sm.kt + swizzled(kD, 32 * fw + 2 * i + 1, t)) = a.y;
+                for (int i = 0; i < 4; ++i) {
+                    uint4 k = *reinterpret_cast<const uint4 *>(rk + 128 * t + ((((fw & 1) * 4 + i) ^ (t & 7)) << 4));
+                    if (t >= m) k = make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const float2 a = widen<BF16>(w[d]);
+                        *reinterpret_cast<float *>(sm.kt + swizzled(kD, 32 * fw + 8 * i + 2 * d, t)) = a.x;
+                        *reinterpret_cast<float *>(sm.kt + swizzled(kD, 32 * fw + 8 * i + 2 * d + 1, t)) = a.y;
+                    }
                 }
             }
             fence_async_smem();
             barrier_arrive(smem_addr(&sm.kt_full));
+            asm volatile("bar.sync 2, 128;" ::: "memory");  // all have read what comes next over it
+            if (ft == 0 && c + 1 < chunks) fetch(c + 1);
+        }
+    } else if (warp >= 13) {
+        // ------------------------------------------------ T, P, and V, R and D of the chunks
+        const int ft = tid - kGroupThreads - kFeedThreads - 32;
+        for (int i = ft; i < kC * kC / 4; i += kSideThreads) {  // above the diagonal they stay zero
+            reinterpret_cast<uint4 *>(sm.t_hi)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.t_lo)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
+        }
+        const auto fetch_tp = [&](int c) {
+            const uint32_t bar = smem_addr(&sm.tp_raw_full);
+            barrier_expect(bar, 2 * kTriangle * 4);
+            bulk_copy(smem_addr(sm.tp_raw), prep[static_cast<size_t>(c) * H].t, 2 * kTriangle * 4, bar);
+        };
+        const auto fetch_v = [&](int c) {
+            const uint32_t bar = smem_addr(&sm.v_full);
+            barrier_expect(bar, 2 * kC * 128 + 2 * kC * 4);
+            for (int half = 0; half < 2; ++half) tma_load3(smem_addr(sm.v[half]), &v_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
+            bulk_copy(smem_addr(&sm.rd[c & 1]), prep[static_cast<size_t>(c) * H].r, 2 * kC * 4, bar);
+        };
+        if (ft == 0) {
+            fetch_v(0);
+            fetch_tp(0);
+        }
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        for (int c = 0; c < chunks && ok; ++c) {
+            ok = barrier_wait(smem_addr(&sm.tp_raw_full), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1));
+            if (!ok) break;
+            // ten blocks each of T and P, ten vectors a thread
+#pragma unroll
+            for (int i = 0; i < 10; ++i) {
+                const int x = ft + kSideThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
+                const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
+                const uint32_t at = swizzled(kC, 16 * bi + in / 16, 16 * bj + in % 16);
+                const float4 tv = *reinterpret_cast<const float4 *>(sm.tp_raw + 4 * x);
+                const float4 hi = make_float4(tf32_hi(tv.x), tf32_hi(tv.y), tf32_hi(tv.z), tf32_hi(tv.w));
+                *reinterpret_cast<float4 *>(sm.t_hi + at) = hi;
+                *reinterpret_cast<float4 *>(sm.t_lo + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
+                *reinterpret_cast<float4 *>(sm.p + at) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
+            }
+            fence_async_smem();
+            barrier_arrive(smem_addr(&sm.tp_full));
+            asm volatile("bar.sync 1, 64;" ::: "memory");  // all have read what comes next over it
+            if (ft == 0 && c + 1 < chunks) {
+                fetch_tp(c + 1);
+                ok = barrier_wait(smem_addr(&sm.v_empty), c & 1);
+                if (ok) fetch_v(c + 1);
+            }
         }
     } else if (warp == 12) {
         // ------------------------------------------------ products
@@ -580,6 +609,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
         // ------------------------------------------------ between the products: a lane is a column of the state
         const int half = warp >> 2, j = (warp & 3) * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint8_t *v = sm.v[j >> 6] + (j & 7) * 2;
         // X_0 and its terms, 32 key rows at a time; x_next: R_63 of the chunk that starts
         const auto put = [&](int col, uint32_t (&x)[32], float x_next) {
             uint32_t w[32];
@@ -593,10 +623,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) * x_next);
             tmem_store32(base + kColX + col, w);
         };
-        ok = barrier_wait(smem_addr(&sm.v_full[0]), 0);
+        ok = barrier_wait(smem_addr(&sm.v_full), 0);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
-            const float x_next = sm.r[0][kC - 1];
+            const float x_next = sm.rd[0].r[kC - 1];
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const int col = 64 * half + 32 * b;
@@ -611,7 +641,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
         }
         for (int c = 0; c < chunks && ok; ++c) {
             const uint32_t phase = c & 1;
-            const int vb = c & 1;
+            const auto &rd = sm.rd[c & 1];
+            const int left = len - c * kC - 32 * half;  // of this thread's tokens
             // V - diag(R) K X_0
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.k_done), phase));
             if (!ok) break;
@@ -622,10 +653,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const int t = 32 * half + i;
-                const float v = fmaf(-sm.r[vb][t], __uint_as_float(x[i]), widen1<BF16>(sm.v[vb][t][j]));
-                x[i] = __float_as_uint(v);
-                w[i] = __float_as_uint(tf32_hi(v));
+                const uint16_t v16 = *reinterpret_cast<const uint16_t *>(v + 128 * t + (((j >> 3 & 7) ^ (t & 7)) << 4));
+                x[i] = __float_as_uint(fmaf(-rd.r[t], __uint_as_float(x[i]), widen1<BF16>(v16)));
             }
+            barrier_arrive(smem_addr(&sm.v_empty));
+            if (left < 32) {  // rows behind the prompt's last are not its own
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i >= left) x[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
             tmem_store32(base + kColLo + 32 * half, w);
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
@@ -644,7 +682,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
             tmem_store32(base + kColLo + 32 * half, w);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float u = sm.d[vb][32 * half + i] * __uint_as_float(x[i]);
+                const float u = rd.d[32 * half + i] * __uint_as_float(x[i]);
                 x[i] = __float_as_uint(u);
                 w[i] = __float_as_uint(tf32_hi(u));
             }
@@ -655,13 +693,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
             tmem_wait_store();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.u_full));
-            barrier_arrive(smem_addr(&sm.v_empty[vb]));
             // the state after the chunk
             float x_next = 0.0f;
             if (c + 1 < chunks) {
-                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.v_full[vb ^ 1]), (c + 1) >> 1 & 1));
+                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.v_full), phase ^ 1));
                 if (!ok) break;
-                x_next = sm.r[vb ^ 1][kC - 1];
+                x_next = sm.rd[phase ^ 1].r[kC - 1];
             }
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.x_done), phase));
             if (!ok) break;
@@ -689,14 +726,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
             tmem_wait_load();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.y_empty));
-            const int m = min(kC, len - c * kC) - 32 * half;
             uint16_t *y = static_cast<uint16_t *>(io.y) + ((first + static_cast<long long>(c) * kC + 32 * half) * H + h) * kD + j;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (i < m) y[static_cast<size_t>(i) * H * kD] = narrow1<BF16>(__uint_as_float(x[i]));
+                if (i < left) y[static_cast<size_t>(i) * H * kD] = narrow1<BF16>(__uint_as_float(x[i]));
         }
     }
-    if (!ok && lane == 0) atomicOr(pool.err, kErrTimeout);
+    if (!ok) {
+        if (lane == 0) atomicOr(pool.err, kErrTimeout);
+        drain();
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 12) {
@@ -708,6 +747,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(PoolView pool, 
 template <bool BF16>
 cudaError_t launch(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
+    CUtensorMap q, k, v;
+    if (!make_map(&q, io.q, io.dtype, io.span.total, p.H, 1, kC) || !make_map(&k, io.k, io.dtype, io.span.total, p.H, 1, kC) ||
+        !make_map(&v, io.v, io.dtype, io.span.total, p.H, 1, kC))
+        return cudaErrorInvalidValue;
     const int prep = static_cast<int>(sizeof(PrepSmem)), smem = static_cast<int>(sizeof(ChunkSmem)) + 1024;
     cudaError_t e = cudaFuncSetAttribute(prepare_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -716,7 +759,7 @@ cudaError_t launch(const PoolView &p, const PromptIO &io, cudaStream_t stream)
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    chunk_kernel<BF16><<<static_cast<unsigned>(io.n) * p.H, kChunkThreads, smem, stream>>>(p, io);
+    chunk_kernel<BF16><<<static_cast<unsigned>(io.n) * p.H, kChunkThreads, smem, stream>>>(q, k, v, p, io);
     count_launch();
     return cudaGetLastError();
 }

@@ -121,7 +121,6 @@ cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t st
 constexpr int kPromptChunk = 64;
 constexpr int kPreparedBytes = 20992;
 constexpr long long prompt_chunks(int n, int total) { return static_cast<long long>(total) / kPromptChunk + n; }  // at most
-bool prompt_in_chunks(int n, int total, int H, int dtype);
 cudaError_t launch_prompt_chunks(const PoolView &p, const PromptIO &io, cudaStream_t stream);
 
 void count_launch();

@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "stq_host.h"
+#include "stq_map.h"
 #include "stq_ptx.h"
 
 namespace stq {
@@ -239,15 +240,14 @@ cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t st
 
 }  // namespace
 
-// 16-bit rows go in chunks unless the prompts are so short that most of a chunk would be empty.
-bool prompt_in_chunks(int n, int total, int H, int dtype)
-{
-    return dtype != STQ_F32 && H <= 65535 && total >= 16ll * n;
-}
-
 cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
-    if (prompt_in_chunks(io.n, io.span.total, p.H, io.dtype)) return launch_prompt_chunks(p, io, stream);
+    // 16-bit rows go in chunks (of rows that a tensor map can describe), unless the prompts are so short that
+    // most of a chunk would be empty
+    const int total = io.span.total;
+    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= 16ll * io.n && rows_mappable(io.q, p.H, total) &&
+        rows_mappable(io.k, p.H, total) && rows_mappable(io.v, p.H, total))
+        return launch_prompt_chunks(p, io, stream);
     const long long units = static_cast<long long>(io.n) * p.H;
     if (units >= 256) return launch_tokens<4>(p, io, stream);
     return units >= 128 ? launch_tokens<8>(p, io, stream) : launch_tokens<16>(p, io, stream);
