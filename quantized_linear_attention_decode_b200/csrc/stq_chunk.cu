@@ -12,9 +12,9 @@
 //
 // Precision.  The state has to come out as the recurrence in fp32 gives it.  k is a
 // 16-bit value, exact in tf32 (11 bits); X_0, V - K X_0, T and D U are fp32 values
-// and enter the tensor core as two tf32 terms, x = hi + lo with hi rounded to
-// nearest, 2^-21 of x left: 2 products against k, 3 of the 4 for T times a vector.  Y
-// is rounded to 16 bits and takes one term of each (2^-11).  Sums are fp32.
+// and enter the tensor core as two tf32 terms, x = hi + lo, 2^-21 of x left: 2 products
+// against k, 3 of the 4 for T times a vector.  Y is rounded to 16 bits and takes one
+// term of each (rounded to nearest, 2^-11).  Sums are fp32.
 #include <cmath>
 
 #include "stq_host.h"
@@ -47,6 +47,9 @@ __device__ __forceinline__ int block_of(int i, int j) { return (i * (i + 1) / 2 
 // x rounded to tf32, to nearest; what is left of it.
 __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
 
+// The same by cutting, for a first term whose rest follows: what the tensor core cuts off the rest is 2^-21 of x.
+__device__ __forceinline__ float tf32_cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+
 // ---------------------------------------------------------------- T and P of every chunk
 
 constexpr int kPrepThreads = 128;
@@ -70,6 +73,19 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr));
 }
 
+// 16 bytes to shared memory, asynchronously; zeros where `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 struct PrepSmem {
     union {
         struct {
@@ -79,8 +95,10 @@ struct PrepSmem {
             float a[kC][kC + 4], t[kC][kC + 4];
         } m;
     };
-    float r[kC][kC + 1];
     float w[3][16][20];
+    float near[8][8][8];         // R_ti within group b: [b][t][i]
+    float mid[8][8];             // products of the groups strictly between two
+    float pre[kC], suf[kC];      // products from the token's group's start through it, and behind it to the group's end
     float alpha[kC], beta[kC];
     int item[3];
 };
@@ -111,11 +129,48 @@ __device__ __forceinline__ bool find_chunk(const PromptIO &io, int chunk, int *e
     return false;
 }
 
-// Bound by the tensor products (2 x 64 x 64 x 128 of 16-bit values) no more than by the
-// inverse: its diagonal blocks of 16 by substitution, a thread a column, the others
-// by block products in fp32.  Four CTAs on an SM hide each other's latencies.
+// The blocks of T at distance D below the diagonal, T_ij = -T_ii sum_{j <= k < i} A_ik T_kj; a thread has two
+// neighbouring elements of each.
+template <int D>
+__device__ __forceinline__ void below(PrepSmem &s)
+{
+    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;
+    float2 w[4 - D];
+#pragma unroll
+    for (int j = 0; j < 4 - D; ++j) w[j] = make_float2(0.0f, 0.0f);
+#pragma unroll 16
+    for (int k = 0; k < 16 * D; ++k)
+#pragma unroll
+        for (int j = 0; j < 4 - D; ++j) {
+            const float a = s.m.a[16 * (j + D) + r][16 * j + k];
+            const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[16 * j + k][16 * j + c]);
+            w[j] = make_float2(fmaf(a, y.x, w[j].x), fmaf(a, y.y, w[j].y));
+        }
+#pragma unroll
+    for (int j = 0; j < 4 - D; ++j) *reinterpret_cast<float2 *>(&s.w[j][r][c]) = w[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4 - D; ++j) w[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 4 - D; ++j) {
+            const float a = -s.m.t[16 * (j + D) + r][16 * (j + D) + k];
+            const float2 y = *reinterpret_cast<const float2 *>(&s.w[j][k][c]);
+            w[j] = make_float2(fmaf(a, y.x, w[j].x), fmaf(a, y.y, w[j].y));
+        }
+#pragma unroll
+    for (int j = 0; j < 4 - D; ++j) *reinterpret_cast<float2 *>(&s.m.t[16 * (j + D) + r][16 * j + c]) = w[j];
+    __syncthreads();
+}
+
+// Bound by the latencies of its steps, five CTAs on an SM hiding each other's, and by
+// shared-memory accesses.  The inverse: its diagonal blocks of 16 by substitution, a thread a
+// column, the others by block products in fp32 (a column of all 64 unknowns a thread took
+// 10 % longer).  R_ti is put together from products within groups of eight tokens and of whole
+// groups between them.
 template <bool BF16>
-__global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, int H)
+__global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, int H)
 {
     extern __shared__ __align__(16) uint8_t raw_smem[];
     PrepSmem &s = *reinterpret_cast<PrepSmem *>(raw_smem);
@@ -135,32 +190,52 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, i
     const long long row0 = io.span.seq_start[e] + static_cast<long long>(s.item[1]) * kC;
     const int m = min(kC, io.span.length(e) - s.item[1] * kC);
     Prepared *out = prepared(io, H, e, s.item[1], h);
-    for (int i = tid; i < kC * kD / 8; i += kPrepThreads) {
-        const int t = i / (kD / 8), d = i % (kD / 8) * 8;
-        uint4 kk = make_uint4(0, 0, 0, 0), qq = kk;
-        if (t < m) {
-            kk = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(io.k.data) + (row0 + t) * io.k.token_stride + h * io.k.head_stride + d);
-            qq = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(io.q.data) + (row0 + t) * io.q.token_stride + h * io.q.head_stride + d);
-        }
-        *reinterpret_cast<uint4 *>(&s.in.k[t][d]) = kk;
-        *reinterpret_cast<uint4 *>(&s.in.q[t][d]) = qq;
+#pragma unroll
+    for (int i = 0; i < kC * kD / 8 / kPrepThreads; ++i) {  // 16 threads a row
+        const int t = tid / 16 + 8 * i, d = tid % 16 * 8;
+        const long long row = row0 + min(t, m - 1);
+        copy16(smem_addr(&s.in.k[t][d]), static_cast<const uint16_t *>(io.k.data) + row * io.k.token_stride + h * io.k.head_stride + d, t < m);
+        copy16(smem_addr(&s.in.q[t][d]), static_cast<const uint16_t *>(io.q.data) + row * io.q.token_stride + h * io.q.head_stride + d, t < m);
     }
     if (tid < kC) {
-        s.alpha[tid] = tid < m ? io.alpha[(row0 + tid) * H + h] : 1.0f;
-        s.beta[tid] = tid < m ? io.beta[(row0 + tid) * H + h] : 0.0f;
+        s.alpha[tid] = 1.0f;
+        s.beta[tid] = 0.0f;
+        if (tid < m) {
+            copy4(smem_addr(&s.alpha[tid]), io.alpha + (row0 + tid) * H + h);
+            copy4(smem_addr(&s.beta[tid]), io.beta + (row0 + tid) * H + h);
+        }
+    }
+    copies_wait();
+    __syncthreads();
+    // products of decays, never quotients: a decay may be zero
+    if (tid < kC) {
+        const int b = tid >> 3, i = tid & 7;
+        float r = 1.0f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {  // column i of the group
+            r = t > i ? r * s.alpha[8 * b + t] : t == i ? 1.0f : 0.0f;
+            s.near[b][t][i] = r;
+        }
+        s.suf[tid] = r;
+        r = 1.0f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) r = t <= i ? r * s.alpha[8 * b + t] : r;
+        s.pre[tid] = r;
     }
     __syncthreads();
-    // R by running products (no logarithms: a decay may be zero or negative)
-    if (tid < kC) {
-        float r = 1.0f;
-        for (int t = tid; t < kC; ++t) {
-            if (t > tid) r *= s.alpha[t];
-            s.r[t][tid] = r;
+    if (tid < 64) {
+        const int hi = tid >> 3, lo = tid & 7;
+        float r = 1.0f, before = 1.0f, behind = 1.0f;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const float all = s.pre[8 * b + 7];
+            if (b > lo && b < hi) r *= all;
+            if (b < hi) before *= all;   // of this thread's token, whose group is hi
+            if (b > hi) behind *= all;
         }
-        out->d[tid] = r;
-    } else if (tid == kC) {
-        float r = 1.0f;
-        for (int t = 0; t < kC; ++t) out->r[t] = r *= s.alpha[t];
+        s.mid[hi][lo] = r;
+        out->r[tid] = before * s.pre[tid];
+        out->d[tid] = s.suf[tid] * behind;
     }
     // k k^T and q k^T, rows 16 warp .. + 15, columns up to the diagonal
     float kk[8][4], qk[8][4];
@@ -186,22 +261,26 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, i
             mma16<BF16>(qk[2 * np + 1], qa, b[2], b[3]);
         }
     }
-    __syncthreads();  // k and q are read, R is there
+    __syncthreads();  // k and q are read, R's parts are there
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
         if (nt / 2 > warp) continue;
+        const float2 suf = *reinterpret_cast<const float2 *>(&s.suf[8 * nt + 2 * t4]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int t = 16 * warp + g + 8 * half, i = 8 * nt + 2 * t4;
-            float a[2], p[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float r = i + j <= t ? s.r[t][i + j] : 0.0f;
-                a[j] = i + j < t ? s.beta[t] * (r * kk[nt][2 * half + j]) : 0.0f;
-                p[j] = i + j <= t ? tf32_hi(r * qk[nt][2 * half + j]) : 0.0f;
+            const int t = 16 * warp + g + 8 * half, i = 8 * nt + 2 * t4, b = 2 * warp + half;
+            float2 r = make_float2(0.0f, 0.0f);
+            if (b == nt) {
+                r = *reinterpret_cast<const float2 *>(&s.near[b][g][2 * t4]);
+            } else if (b > nt) {
+                const float through = s.mid[b][nt] * s.pre[t];
+                r = make_float2(suf.x * through, suf.y * through);
             }
-            *reinterpret_cast<float2 *>(&s.m.a[t][i]) = make_float2(a[0], a[1]);
-            *reinterpret_cast<float2 *>(out->p + block_of(warp, nt / 2) + (t & 15) * 16 + (i & 15)) = make_float2(p[0], p[1]);
+            const float beta = s.beta[t];
+            const float2 a = make_float2(i < t ? beta * (r.x * kk[nt][2 * half]) : 0.0f, i + 1 < t ? beta * (r.y * kk[nt][2 * half + 1]) : 0.0f);
+            const float2 p = make_float2(i <= t ? tf32_hi(r.x * qk[nt][2 * half]) : 0.0f, i + 1 <= t ? tf32_hi(r.y * qk[nt][2 * half + 1]) : 0.0f);
+            *reinterpret_cast<float2 *>(&s.m.a[t][i]) = a;
+            *reinterpret_cast<float2 *>(out->p + block_of(warp, nt / 2) + (t & 15) * 16 + (i & 15)) = p;
         }
     }
     __syncthreads();
@@ -220,41 +299,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4) prepare_kernel(PromptIO io, i
         for (int i = 0; i < 16; ++i) s.m.t[16 * b + i][16 * b + c] = x[i];
     }
     __syncthreads();
-    // T_ij = -T_ii sum_{j <= k < i} A_ik T_kj, by distance from the diagonal
-    const int r = tid >> 3, c = (tid & 7) * 2;
-    for (int dist = 1; dist < 4; ++dist) {
-        for (int j = 0; j + dist < 4; ++j) {
-            const int i = j + dist;
-            float2 w = make_float2(0.0f, 0.0f);
-            for (int k = 16 * j; k < 16 * i; ++k) {
-                const float a = s.m.a[16 * i + r][k];
-                const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[k][16 * j + c]);
-                w = make_float2(fmaf(a, y.x, w.x), fmaf(a, y.y, w.y));
-            }
-            *reinterpret_cast<float2 *>(&s.w[j][r][c]) = w;
-        }
-        __syncthreads();
-        for (int j = 0; j + dist < 4; ++j) {
-            const int i = j + dist;
-            float2 w = make_float2(0.0f, 0.0f);
+    below<1>(s);
+    below<2>(s);
+    below<3>(s);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = -s.m.t[16 * i + r][16 * i + k];
-                const float2 y = *reinterpret_cast<const float2 *>(&s.w[j][k][c]);
-                w = make_float2(fmaf(a, y.x, w.x), fmaf(a, y.y, w.y));
-            }
-            *reinterpret_cast<float2 *>(&s.m.t[16 * i + r][16 * j + c]) = w;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) {
+            const int t = 16 * i + (tid >> 3), col = 16 * j + (tid & 7) * 2;
+            const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[t][col]);
+            *reinterpret_cast<float2 *>(out->t + block_of(i, j) + 2 * tid) = make_float2(y.x * s.beta[col], y.y * s.beta[col + 1]);
         }
-        __syncthreads();
-    }
-    for (int x = tid; x < kTriangle / 2; x += kPrepThreads) {
-        const int blk = x / (kBlockFloats / 2), in = x % (kBlockFloats / 2) * 2;
-        int i = 0;
-        while ((i + 1) * (i + 2) / 2 <= blk) ++i;
-        const int j = blk - i * (i + 1) / 2, t = 16 * i + in / 16, col = 16 * j + in % 16;
-        const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[t][col]);
-        *reinterpret_cast<float2 *>(out->t + 2 * x) = make_float2(y.x * s.beta[col], y.y * s.beta[col + 1]);
-    }
 }
 
 // ---------------------------------------------------------------- the walk over the chunks
@@ -639,38 +694,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.x_full));
         }
+        uint32_t ys[16];  // the last chunk's Y, two tokens a register, until there is time to store it
+        const auto store_y = [&](int c) {
+            const int left = len - c * kC - 32 * half;
+            uint16_t *y = static_cast<uint16_t *>(io.y) + ((first + static_cast<long long>(c) * kC + 32 * half) * H + h) * kD + j;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < left) y[static_cast<size_t>(i) * H * kD] = static_cast<uint16_t>(ys[i >> 1] >> (16 * (i & 1)));
+        };
         for (int c = 0; c < chunks && ok; ++c) {
             const uint32_t phase = c & 1;
             const auto &rd = sm.rd[c & 1];
             const int left = len - c * kC - 32 * half;  // of this thread's tokens
-            // V - diag(R) K X_0
-            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.k_done), phase));
-            if (!ok) break;
-            tc_fence_after();
             uint32_t x[32], w[32];
-            tmem_load32(base + kColK + 32 * half, x);
-            tmem_wait_load();
+            // V - diag(R) K X_0
+            float vs[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const int t = 32 * half + i;
-                const uint16_t v16 = *reinterpret_cast<const uint16_t *>(v + 128 * t + (((j >> 3 & 7) ^ (t & 7)) << 4));
-                x[i] = __float_as_uint(fmaf(-rd.r[t], __uint_as_float(x[i]), widen1<BF16>(v16)));
+                vs[i] = widen1<BF16>(*reinterpret_cast<const uint16_t *>(v + 128 * t + (((j >> 3 & 7) ^ (t & 7)) << 4)));
             }
             barrier_arrive(smem_addr(&sm.v_empty));
+            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.k_done), phase));
+            if (!ok) break;
+            tc_fence_after();
+            tmem_load32(base + kColK + 32 * half, x);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) vs[i] = fmaf(-rd.r[32 * half + i], __uint_as_float(x[i]), vs[i]);
             if (left < 32) {  // rows behind the prompt's last are not its own
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (i >= left) x[i] = 0u;
+                    if (i >= left) vs[i] = 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_cut(vs[i]));
             tmem_store32(base + kColLo + 32 * half, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
-            tmem_store32(base + kColLo + 64 + 32 * half, w);
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(vs[i] - __uint_as_float(w[i]));
+            tmem_store32(base + kColLo + 64 + 32 * half, x);
             tmem_wait_store();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.r_full));
+            if (c > 0) store_y(c - 1);
             // U, and D U
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.u_done), phase));
             if (!ok) break;
@@ -682,14 +748,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tmem_store32(base + kColLo + 32 * half, w);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float u = rd.d[32 * half + i] * __uint_as_float(x[i]);
-                x[i] = __float_as_uint(u);
-                w[i] = __float_as_uint(tf32_hi(u));
+                x[i] = __float_as_uint(rd.d[32 * half + i] * __uint_as_float(x[i]));
+                w[i] = __float_as_uint(tf32_cut(__uint_as_float(x[i])));
             }
             tmem_store32(base + kColHi + 32 * half, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
-            tmem_store32(base + kColHi + 64 + 32 * half, w);
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
+            tmem_store32(base + kColHi + 64 + 32 * half, x);
             tmem_wait_store();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.u_full));
@@ -718,7 +783,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tmem_wait_store();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.x_full));
-            // Y, while the next chunk's first products run
+            // Y (its products came before the state's)
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.y_done), phase));
             if (!ok) break;
             tc_fence_after();
@@ -726,11 +791,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tmem_wait_load();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.y_empty));
-            uint16_t *y = static_cast<uint16_t *>(io.y) + ((first + static_cast<long long>(c) * kC + 32 * half) * H + h) * kD + j;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left) y[static_cast<size_t>(i) * H * kD] = narrow1<BF16>(__uint_as_float(x[i]));
+            for (int i = 0; i < 16; ++i)
+                ys[i] = narrow1<BF16>(__uint_as_float(x[2 * i])) | static_cast<uint32_t>(narrow1<BF16>(__uint_as_float(x[2 * i + 1]))) << 16;
         }
+        if (ok) store_y(chunks - 1);
     }
     if (!ok) {
         if (lane == 0) atomicOr(pool.err, kErrTimeout);

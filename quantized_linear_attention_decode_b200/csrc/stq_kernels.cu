@@ -40,7 +40,10 @@ __device__ __forceinline__ uint8_t *tile_page(const PoolView &p, int req, int sl
 // codes are taken with the table's c, then every column is refitted over the
 // non-pivot rows in fp64, c_j = sum_i w_i^2 v_ij S_ij / sum_i w_i^2 v_ij^2 with
 // v_ij = s_i r_i z_ij (each term formed in the oracle's operation order), and
-// stored in the page.  One warp per row.
+// stored in the page.  One warp per row; without the fit a tile's rows do not meet, and
+// kQuantizeCtas CTAs share them (768 tiles: 75 us with one CTA a tile and every quotient
+// divided, 4 tiles 26 us).
+constexpr int kQuantizeCtas = 4;
 __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t *req_idx,
                                                        const int32_t *slot_idx, const float *state, PromptSpan span)
 {
@@ -62,18 +65,35 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
     const float *wrow = p.t.w + static_cast<size_t>(h) * kD;
     double fnum[4] = {0.0, 0.0, 0.0, 0.0}, fden[4] = {0.0, 0.0, 0.0, 0.0};
     bool bad = false;
-    for (int i = warp; i < kD; i += 8) {
-        const int b = p.t.row_bits[h * kD + i];
+    // the next row is loaded while this one is quantized
+    int next_b;
+    float next_r;
+    float4 next_x;
+    uint32_t next_off;
+    const auto fetch = [&](int i) {
+        next_b = p.t.row_bits[h * kD + i];
+        next_r = p.t.r[h * kD + i];
+        next_off = p.t.row_off[h * kD + i];
+        next_x = *reinterpret_cast<const float4 *>(S + i * kD + lane * 4);
+    };
+    fetch(warp + 8 * blockIdx.y);
+    for (int i = warp + 8 * blockIdx.y; i < kD; i += 8 * gridDim.y) {
+        const int b = next_b;
         const int qb = qmax_of(b);
-        const double r = static_cast<double>(p.t.r[h * kD + i]);
-        const float4 x4 = *reinterpret_cast<const float4 *>(S + i * kD + lane * 4);
+        const float rf = next_r;
+        const double r = static_cast<double>(rf);
+        const float4 x4 = next_x;
+        const uint32_t off = next_off;
+        if (i + 8 * static_cast<int>(gridDim.y) < kD) fetch(i + 8 * gridDim.y);
         const float x[4] = {x4.x, x4.y, x4.z, x4.w};
         float mu[4];
         float a = 0.0f;
         const bool pivot_fit = b == 16 && p.fit;  // a fitted page's pivot row leaves c out
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            mu[t] = static_cast<float>(static_cast<double>(x[t]) / (pivot_fit ? r : r * static_cast<double>(cj[t])));
+            // a division by one would change nothing
+            if (rf == 1.0f && (pivot_fit || cj[t] == 1.0f)) mu[t] = x[t];
+            else mu[t] = static_cast<float>(static_cast<double>(x[t]) / (pivot_fit ? r : r * static_cast<double>(cj[t])));
             a = fmaxf(a, fabsf(mu[t]));
             bad |= !isfinite(x[t]);
         }
@@ -84,7 +104,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
             uint2 w;
             w.x = *reinterpret_cast<const uint32_t *>(&h01);
             w.y = *reinterpret_cast<const uint32_t *>(&h23);
-            *reinterpret_cast<uint2 *>(page + p.t.row_off[h * kD + i] + lane * 8) = w;
+            *reinterpret_cast<uint2 *>(page + off + lane * 8) = w;
             const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
             bad |= !(isfinite(f01.x) && isfinite(f01.y) && isfinite(f23.x) && isfinite(f23.y));
             if (lane == 0) {
@@ -108,7 +128,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
             }
             code[t] = static_cast<uint32_t>(zz);
         }
-        uint8_t *row = page + p.t.row_off[h * kD + i];
+        uint8_t *row = page + off;
         if (b == 8) {
             *reinterpret_cast<uint32_t *>(row + lane * 4) = (code[0] & 255u) | (code[1] & 255u) << 8 |
                                                             (code[2] & 255u) << 16 | (code[3] & 255u) << 24;
@@ -315,7 +335,7 @@ cudaError_t launch_quantize(const PoolView &p, const int32_t *req_idx, const int
 {
     if (p.raw_bits == 32) quantize_raw_kernel<32><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     else if (p.raw_bits == 16) quantize_raw_kernel<16><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
-    else quantize_kernel<<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else quantize_kernel<<<dim3(n * p.H, p.fit ? 1 : kQuantizeCtas), 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     count_launch();
     return cudaGetLastError();
 }
