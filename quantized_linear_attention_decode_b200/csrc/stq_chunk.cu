@@ -129,45 +129,77 @@ __device__ __forceinline__ bool find_chunk(const PromptIO &io, int chunk, int *e
     return false;
 }
 
-// The blocks of T at distance D below the diagonal, T_ij = -T_ii sum_{j <= k < i} A_ik T_kj; a thread has two
-// neighbouring elements of each.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], float b0, float b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+// d += a b of fp32 16 x 16 and 16 x 8 blocks (rows of `pitch` floats), each factor in two tf32 terms, three products.
+__device__ __forceinline__ void block_product(float (&d)[4], const float *a, const float *b, int pitch_a, int pitch_b)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 16; k += 8) {
+        float x[4], xh[4], xl[4], y[2], yh[2], yl[2];
+        x[0] = a[g * pitch_a + k + t4];
+        x[1] = a[(g + 8) * pitch_a + k + t4];
+        x[2] = a[g * pitch_a + k + t4 + 4];
+        x[3] = a[(g + 8) * pitch_a + k + t4 + 4];
+        y[0] = b[(k + t4) * pitch_b + g];
+        y[1] = b[(k + t4 + 4) * pitch_b + g];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            xh[i] = tf32_hi(x[i]);
+            xl[i] = x[i] - xh[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            yh[i] = tf32_hi(y[i]);
+            yl[i] = y[i] - yh[i];
+        }
+        mma_tf32(d, xl, yh[0], yh[1]);
+        mma_tf32(d, xh, yl[0], yl[1]);
+        mma_tf32(d, xh, yh[0], yh[1]);
+    }
+}
+
+// The blocks of T at distance D below the diagonal, T_ij = -T_ii sum_{j <= k < i} A_ik T_kj, in halves of
+// eight columns dealt to the warps.
 template <int D>
 __device__ __forceinline__ void below(PrepSmem &s)
 {
-    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;
-    float2 w[4 - D];
+    constexpr int kPitch = kC + 4, kPitchW = 20;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 4 - D; ++j) w[j] = make_float2(0.0f, 0.0f);
-#pragma unroll 16
-    for (int k = 0; k < 16 * D; ++k)
+    for (int x = 0; x < 2 * (4 - D); x += 4) {
+        const int j = (x + warp) >> 1, c = (x + warp & 1) * 8, i = j + D;
+        if (j >= 4 - D) continue;
+        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 4 - D; ++j) {
-            const float a = s.m.a[16 * (j + D) + r][16 * j + k];
-            const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[16 * j + k][16 * j + c]);
-            w[j] = make_float2(fmaf(a, y.x, w[j].x), fmaf(a, y.y, w[j].y));
-        }
-#pragma unroll
-    for (int j = 0; j < 4 - D; ++j) *reinterpret_cast<float2 *>(&s.w[j][r][c]) = w[j];
+        for (int k = 0; k < D; ++k) block_product(w, &s.m.a[16 * i][16 * (j + k)], &s.m.t[16 * (j + k)][16 * j + c], kPitch, kPitch);
+        *reinterpret_cast<float2 *>(&s.w[j][g][c + 2 * t4]) = make_float2(w[0], w[1]);
+        *reinterpret_cast<float2 *>(&s.w[j][g + 8][c + 2 * t4]) = make_float2(w[2], w[3]);
+    }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4 - D; ++j) w[j] = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-        for (int j = 0; j < 4 - D; ++j) {
-            const float a = -s.m.t[16 * (j + D) + r][16 * (j + D) + k];
-            const float2 y = *reinterpret_cast<const float2 *>(&s.w[j][k][c]);
-            w[j] = make_float2(fmaf(a, y.x, w[j].x), fmaf(a, y.y, w[j].y));
-        }
-#pragma unroll
-    for (int j = 0; j < 4 - D; ++j) *reinterpret_cast<float2 *>(&s.m.t[16 * (j + D) + r][16 * j + c]) = w[j];
+    for (int x = 0; x < 2 * (4 - D); x += 4) {
+        const int j = (x + warp) >> 1, c = (x + warp & 1) * 8, i = j + D;
+        if (j >= 4 - D) continue;
+        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        block_product(w, &s.m.t[16 * i][16 * i], &s.w[j][0][c], kPitch, kPitchW);
+        *reinterpret_cast<float2 *>(&s.m.t[16 * i + g][16 * j + c + 2 * t4]) = make_float2(-w[0], -w[1]);
+        *reinterpret_cast<float2 *>(&s.m.t[16 * i + g + 8][16 * j + c + 2 * t4]) = make_float2(-w[2], -w[3]);
+    }
     __syncthreads();
 }
 
 // Bound by the latencies of its steps, five CTAs on an SM hiding each other's, and by
 // shared-memory accesses.  The inverse: its diagonal blocks of 16 by substitution, a thread a
-// column, the others by block products in fp32 (a column of all 64 unknowns a thread took
-// 10 % longer).  R_ti is put together from products within groups of eight tokens and of whole
+// column, the others by block products in three tf32 terms (in fp32 on the other pipe they
+// took four times the accesses).  R_ti is put together from products within groups of eight tokens and of whole
 // groups between them.
 template <bool BF16>
 __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, int H)
@@ -320,12 +352,15 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
 // (K, Q, K^T, T, P, as fp32 in 128-byte swizzled rows) are written to shared memory by six
 // warps that run ahead.  Columns of tensor memory:
 //     0  X^T, the sum that the chunk's update goes onto, scaled by R_63 beforehand
-//   128  X_0^T hi; after the products with K and Q: (D U)^T hi | lo
-//   256  X_0^T lo; after the product with K: (V - R K X_0)^T hi | lo; after T: U^T hi
-//   384  (K X_0)^T; then U^T
+//   128  X_0^T hi; then (T (V - R K X_0))^T in two parts; then (D U)^T hi | lo
+//   256  X_0^T lo; then (V - R K X_0)^T hi | lo
+//   384  (K X_0)^T; then U^T hi
 //   448  (diag(R) Q X_0)^T, then Y^T
-// Bound by the chain of a chunk's products and what stands between them: 3200 cycles
-// of products, of which all but Y's are in a row.
+// A product of 8 deep takes 64 cycles whatever its width up to 128 columns, for its A
+// operand's sake, so K and Q stand under each other for the hi term, and T's two terms for
+// theirs: 16 x 128 and 16 x 64 for K and Q, 8 x 128 and 8 x 64 for T, 16 x 128 for the update,
+// 8 x 64 for Y's, 4600 cycles.  Bound by the chain of all but Y's with what stands
+// between them.
 
 constexpr int kGroupThreads = 256;  // warps 0-7: two for each quarter of the lanes, half of the columns each
 constexpr int kFeedThreads = 128;   // warps 8-11; warp 12 issues the products
@@ -334,16 +369,17 @@ constexpr int kChunkThreads = kGroupThreads + kFeedThreads + 32 + kSideThreads;
 constexpr uint32_t kColX = 0, kColHi = 128, kColLo = 256, kColK = 384, kColY = 448;
 
 struct __align__(1024) ChunkSmem {
-    uint8_t k[kC * kD * 4], q[kC * kD * 4];   // 4 blocks of 32 dims: 64 rows of 128 bytes
-    uint8_t kt[kC * kD * 4];                  // 2 blocks of 32 tokens: 128 rows
-    uint8_t t_hi[kC * kC * 4], t_lo[kC * kC * 4], p[kC * kC * 4];  // 2 blocks of 32 tokens: 64 rows
+    uint8_t kq[2 * kC * kD * 4];  // 4 blocks of 32 dims: 128 rows of 128 bytes, K's and Q's
+    uint8_t kt[kC * kD * 4];      // 2 blocks of 32 tokens: 128 rows
+    uint8_t t[2 * kC * kC * 4];   // 2 blocks of 32 tokens: 128 rows, T's hi and lo
+    uint8_t p[kC * kC * 4];       // 2 blocks of 32 tokens: 64 rows
     uint8_t raw_k[2][kC * 128], raw_q[2][kC * 128], v[2][kC * 128];  // as they come: 64 dims, 128-byte swizzled rows
     float tp_raw[2 * kTriangle];
     struct {
         float r[kC], d[kC];
     } rd[2];
     unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, tp_full, tp_empty, v_full, v_empty;
-    unsigned long long x_full, k_done, r_full, u_done, u_full, y_done, y_empty, x_done;
+    unsigned long long x_full, k_done, r_full, u_done, u_full, y_done, x_done;
     uint32_t tmem;
     int item[4];
 };
@@ -451,7 +487,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             init(sm.u_done, 1);
             init(sm.u_full, kGroupThreads);
             init(sm.y_done, 1);
-            init(sm.y_empty, kGroupThreads);
             init(sm.x_done, 1);
             fence_barrier_init();
         }
@@ -502,14 +537,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     const int at = 128 * t + ((((fw & 1) * 4 + i) ^ (t & 7)) << 4);
                     uint4 k = *reinterpret_cast<const uint4 *>(rk + at), q = *reinterpret_cast<const uint4 *>(rq + at);
                     if (t >= m) k = q = make_uint4(0, 0, 0, 0);
-                    const uint32_t to0 = swizzled(kC, t, 32 * fw + 8 * i), to1 = swizzled(kC, t, 32 * fw + 8 * i + 4);
+                    const uint32_t to0 = swizzled(2 * kC, t, 32 * fw + 8 * i), to1 = swizzled(2 * kC, t, 32 * fw + 8 * i + 4);
                     const float2 k0 = widen<BF16>(k.x), k1 = widen<BF16>(k.y), k2 = widen<BF16>(k.z), k3 = widen<BF16>(k.w);
-                    *reinterpret_cast<float4 *>(sm.k + to0) = make_float4(k0.x, k0.y, k1.x, k1.y);
-                    *reinterpret_cast<float4 *>(sm.k + to1) = make_float4(k2.x, k2.y, k3.x, k3.y);
+                    *reinterpret_cast<float4 *>(sm.kq + to0) = make_float4(k0.x, k0.y, k1.x, k1.y);
+                    *reinterpret_cast<float4 *>(sm.kq + to1) = make_float4(k2.x, k2.y, k3.x, k3.y);
                     const float2 q0 = widen<BF16>(q.x), q1 = widen<BF16>(q.y), q2 = widen<BF16>(q.z), q3 = widen<BF16>(q.w);
                     const float r = rt[pass];
-                    *reinterpret_cast<float4 *>(sm.q + to0) = make_float4(tf32_hi(q0.x * r), tf32_hi(q0.y * r), tf32_hi(q1.x * r), tf32_hi(q1.y * r));
-                    *reinterpret_cast<float4 *>(sm.q + to1) = make_float4(tf32_hi(q2.x * r), tf32_hi(q2.y * r), tf32_hi(q3.x * r), tf32_hi(q3.y * r));
+                    *reinterpret_cast<float4 *>(sm.kq + kC * 128 + to0) = make_float4(tf32_hi(q0.x * r), tf32_hi(q0.y * r), tf32_hi(q1.x * r), tf32_hi(q1.y * r));
+                    *reinterpret_cast<float4 *>(sm.kq + kC * 128 + to1) = make_float4(tf32_hi(q2.x * r), tf32_hi(q2.y * r), tf32_hi(q3.x * r), tf32_hi(q3.y * r));
                 }
             }
             fence_async_smem();
@@ -542,8 +577,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // ------------------------------------------------ T, P, and V, R and D of the chunks
         const int ft = tid - kGroupThreads - kFeedThreads - 32;
         for (int i = ft; i < kC * kC / 4; i += kSideThreads) {  // above the diagonal they stay zero
-            reinterpret_cast<uint4 *>(sm.t_hi)[i] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4 *>(sm.t_lo)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.t)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.t)[i + kC * kC / 4] = make_uint4(0, 0, 0, 0);
             reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
         }
         const auto fetch_tp = [&](int c) {
@@ -570,12 +605,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int i = 0; i < 10; ++i) {
                 const int x = ft + kSideThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
                 const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
-                const uint32_t at = swizzled(kC, 16 * bi + in / 16, 16 * bj + in % 16);
+                const int row = 16 * bi + in / 16, col = 16 * bj + in % 16;
+                const uint32_t at = swizzled(2 * kC, row, col);
                 const float4 tv = *reinterpret_cast<const float4 *>(sm.tp_raw + 4 * x);
                 const float4 hi = make_float4(tf32_hi(tv.x), tf32_hi(tv.y), tf32_hi(tv.z), tf32_hi(tv.w));
-                *reinterpret_cast<float4 *>(sm.t_hi + at) = hi;
-                *reinterpret_cast<float4 *>(sm.t_lo + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
-                *reinterpret_cast<float4 *>(sm.p + at) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
+                *reinterpret_cast<float4 *>(sm.t + at) = hi;
+                *reinterpret_cast<float4 *>(sm.t + kC * 128 + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
+                *reinterpret_cast<float4 *>(sm.p + swizzled(kC, row, col)) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
             }
             fence_async_smem();
             barrier_arrive(smem_addr(&sm.tp_full));
@@ -589,8 +625,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     } else if (warp == 12) {
         // ------------------------------------------------ products
         constexpr uint32_t n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
-        const uint32_t k = smem_addr(sm.k), q = smem_addr(sm.q), kt = smem_addr(sm.kt);
-        const uint32_t th = smem_addr(sm.t_hi), tl = smem_addr(sm.t_lo), p = smem_addr(sm.p);
+        const uint32_t kq = smem_addr(sm.kq), kt = smem_addr(sm.kt), tt = smem_addr(sm.t), p = smem_addr(sm.p);
+        // step s of 8 in an operand of blocks of 32 columns and `rows` rows
+        const auto step = [](uint32_t base, int rows, int s) { return tc_desc(base + (s >> 2) * rows * 128 + (s & 3) * 32, 16, 1024); };
         for (int c = 0; c < chunks && ok; ++c) {
             const uint32_t phase = c & 1;
             ok = barrier_wait(smem_addr(&sm.kq_full), phase) && barrier_wait(smem_addr(&sm.x_full), phase);
@@ -598,20 +635,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int term = 0; term < 2; ++term)
+                for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColK, tmem + kColHi + 8 * s, step(kq, 128, s), n128, s > 0);
 #pragma unroll
-                    for (int s = 0; s < 16; ++s)
-                        tc_mma_tf32(tmem + kColK, tmem + (term ? kColLo : kColHi) + 8 * s, tc_desc(k + (s >> 2) * 8192 + (s & 3) * 32, 16, 1024), n64, term > 0 || s > 0);
+                for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColK, tmem + kColLo + 8 * s, step(kq, 128, s), n64, true);
                 tc_commit(smem_addr(&sm.k_done));
-            }
-            __syncwarp();
-            if (c > 0) ok = barrier_wait(smem_addr(&sm.y_empty), phase ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < 16; ++s)
-                    tc_mma_tf32(tmem + kColY, tmem + kColHi + 8 * s, tc_desc(q + (s >> 2) * 8192 + (s & 3) * 32, 16, 1024), n64, s > 0);
                 tc_commit(smem_addr(&sm.kq_empty));
             }
             __syncwarp();
@@ -619,16 +646,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                // rows of T from the step's own block of 16 on: those before it have zeros there
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
+                for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 8 * s, step(tt, 128, s), n128, s > 0);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        const int b = s >> 1;
-                        tc_mma_tf32(tmem + kColK + 16 * b, tmem + kColLo + (term == 2 ? 64 : 0) + 8 * s,
-                                    tc_desc((term == 1 ? tl : th) + (s >> 2) * 8192 + (s & 3) * 32 + b * 2048, 16, 1024),
-                                    tc_idesc(2, 128, 64 - 16 * b, false), term > 0 || s > 0);
-                    }
+                for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 64 + 8 * s, step(tt, 128, s), n64, true);
                 tc_commit(smem_addr(&sm.u_done));
             }
             __syncwarp();
@@ -637,20 +658,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const int b = s >> 1;
-                    tc_mma_tf32(tmem + kColY + 16 * b, tmem + kColLo + 8 * s, tc_desc(p + (s >> 2) * 8192 + (s & 3) * 32 + b * 2048, 16, 1024),
-                                tc_idesc(2, 128, 64 - 16 * b, false), true);
-                }
-                tc_commit(smem_addr(&sm.y_done));
-                tc_commit(smem_addr(&sm.tp_empty));
-#pragma unroll
-                for (int term = 0; term < 2; ++term)
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        tc_mma_tf32(tmem + kColX, tmem + kColHi + 64 * term + 8 * s, tc_desc(kt + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024), n128, true);
+                for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColX, tmem + kColHi + 8 * s, step(kt, 128, s & 7), n128, true);
                 tc_commit(smem_addr(&sm.x_done));
                 tc_commit(smem_addr(&sm.kt_empty));
+#pragma unroll
+                for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColY, tmem + kColK + 8 * s, step(p, 64, s), n64, true);
+                tc_commit(smem_addr(&sm.y_done));
+                tc_commit(smem_addr(&sm.tp_empty));
             }
             __syncwarp();
         }
@@ -697,10 +711,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         uint32_t ys[16];  // the last chunk's Y, two tokens a register, until there is time to store it
         const auto store_y = [&](int c) {
             const int left = len - c * kC - 32 * half;
-            uint16_t *y = static_cast<uint16_t *>(io.y) + ((first + static_cast<long long>(c) * kC + 32 * half) * H + h) * kD + j;
+            // two exchanges between lanes give each 4 columns of 8 tokens: 8-byte stores, and a quarter as many
+            const bool odd = lane & 1, two = lane & 2;
+            uint32_t pairs[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left) y[static_cast<size_t>(i) * H * kD] = static_cast<uint16_t>(ys[i >> 1] >> (16 * (i & 1)));
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t mine = odd ? ys[8 + i] : ys[i], other = __shfl_xor_sync(0xffffffffu, odd ? ys[i] : ys[8 + i], 1);
+                const uint32_t a = odd ? other : mine, b = odd ? mine : other;
+                pairs[2 * i] = __byte_perm(a, b, 0x5410);
+                pairs[2 * i + 1] = __byte_perm(a, b, 0x7632);
+            }
+            const int t0 = (odd ? 16 : 0) + (two ? 8 : 0);
+            uint16_t *y = static_cast<uint16_t *>(io.y) + ((first + static_cast<long long>(c) * kC + 32 * half + t0) * H + h) * kD + (j & ~3);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t mine = two ? pairs[8 + i] : pairs[i], other = __shfl_xor_sync(0xffffffffu, two ? pairs[i] : pairs[8 + i], 2);
+                if (t0 + i < left) *reinterpret_cast<uint2 *>(y + static_cast<size_t>(i) * H * kD) = two ? make_uint2(other, mine) : make_uint2(mine, other);
+            }
         };
         for (int c = 0; c < chunks && ok; ++c) {
             const uint32_t phase = c & 1;
@@ -741,11 +768,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.u_done), phase));
             if (!ok) break;
             tc_fence_after();
-            tmem_load32(base + kColK + 32 * half, x);
+            tmem_load32(base + kColHi + 32 * half, x);
+            tmem_load32(base + kColHi + 64 + 32 * half, w);
             tmem_wait_load();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
-            tmem_store32(base + kColLo + 32 * half, w);
+            for (int i = 0; i < 32; ++i) {
+                x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(w[i]));
+                w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
+            }
+            tmem_store32(base + kColK + 32 * half, w);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 x[i] = __float_as_uint(rd.d[32 * half + i] * __uint_as_float(x[i]));
@@ -780,17 +811,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     for (int i = 0; i < 32; ++i) state[static_cast<size_t>(col + i) * kD + j] = __uint_as_float(x[i]);
                 }
             }
-            tmem_wait_store();
-            tc_fence_before();
-            barrier_arrive(smem_addr(&sm.x_full));
-            // Y (its products came before the state's)
+            // Y, whose products come behind the state's; the next chunk's go where it is
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.y_done), phase));
             if (!ok) break;
             tc_fence_after();
             tmem_load32(base + kColY + 32 * half, x);
             tmem_wait_load();
+            tmem_wait_store();
             tc_fence_before();
-            barrier_arrive(smem_addr(&sm.y_empty));
+            barrier_arrive(smem_addr(&sm.x_full));
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 ys[i] = narrow1<BF16>(__uint_as_float(x[2 * i])) | static_cast<uint32_t>(narrow1<BF16>(__uint_as_float(x[2 * i + 1]))) << 16;
