@@ -50,6 +50,15 @@ __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__fl
 // The same by cutting, for a first term whose rest follows: what the tensor core cuts off the rest is 2^-21 of x.
 __device__ __forceinline__ float tf32_cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
 
+// Two neighbouring registers of a row as a pair, for packed arithmetic.
+__device__ __forceinline__ float2 pair_at(const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); }
+__device__ __forceinline__ void put_pair(uint32_t *x, float2 y)
+{
+    x[0] = __float_as_uint(y.x);
+    x[1] = __float_as_uint(y.y);
+}
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.0f, -1.0f), a); }
+
 // ---------------------------------------------------------------- T and P of every chunk
 
 constexpr int kPrepThreads = 128;
@@ -365,7 +374,10 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
 constexpr int kGroupThreads = 256;  // warps 0-7: two for each quarter of the lanes, half of the columns each
 constexpr int kFeedThreads = 128;   // warps 8-11; warp 12 issues the products
 constexpr int kSideThreads = 64;    // warps 13 and 14
-constexpr int kChunkThreads = kGroupThreads + kFeedThreads + 32 + kSideThreads;
+constexpr int kChunkThreads = 512;  // four warpgroups; warp 15 only hands its registers over
+// registers a thread: 128 at launch and in warps 8-11, then 152 in warps 0-7 and 80 in the last four
+// (2 * 152 + 128 + 80 = 4 * 128); where a branch spills instead, the walk takes up to twice as long
+constexpr int kGroupRegs = 152, kOtherRegs = 80;
 constexpr uint32_t kColX = 0, kColHi = 128, kColLo = 256, kColK = 384, kColY = 448;
 
 struct __align__(1024) ChunkSmem {
@@ -379,7 +391,7 @@ struct __align__(1024) ChunkSmem {
         float r[kC], d[kC];
     } rd[2];
     unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, tp_full, tp_empty, v_full, v_empty;
-    unsigned long long x_full, k_done, r_full, u_done, u_full, y_done, x_done;
+    unsigned long long x_full[2], k_done, r_full, u_done, u_full, y_done, x_done;
     uint32_t tmem;
     int item[4];
 };
@@ -481,7 +493,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             init(sm.tp_raw_full, 1);
             init(sm.v_full, 1);
             init(sm.v_empty, kGroupThreads);
-            init(sm.x_full, kGroupThreads);
+            init(sm.x_full[0], kGroupThreads);
+            init(sm.x_full[1], kGroupThreads);
             init(sm.k_done, 1);
             init(sm.r_full, kGroupThreads);
             init(sm.u_done, 1);
@@ -573,109 +586,127 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             asm volatile("bar.sync 2, 128;" ::: "memory");  // all have read what comes next over it
             if (ft == 0 && c + 1 < chunks) fetch(c + 1);
         }
-    } else if (warp >= 13) {
-        // ------------------------------------------------ T, P, and V, R and D of the chunks
-        const int ft = tid - kGroupThreads - kFeedThreads - 32;
-        for (int i = ft; i < kC * kC / 4; i += kSideThreads) {  // above the diagonal they stay zero
-            reinterpret_cast<uint4 *>(sm.t)[i] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4 *>(sm.t)[i + kC * kC / 4] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
-        }
-        const auto fetch_tp = [&](int c) {
-            const uint32_t bar = smem_addr(&sm.tp_raw_full);
-            barrier_expect(bar, 2 * kTriangle * 4);
-            bulk_copy(smem_addr(sm.tp_raw), prep[static_cast<size_t>(c) * H].t, 2 * kTriangle * 4, bar);
-        };
-        const auto fetch_v = [&](int c) {
-            const uint32_t bar = smem_addr(&sm.v_full);
-            barrier_expect(bar, 2 * kC * 128 + 2 * kC * 4);
-            for (int half = 0; half < 2; ++half) tma_load3(smem_addr(sm.v[half]), &v_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
-            bulk_copy(smem_addr(&sm.rd[c & 1]), prep[static_cast<size_t>(c) * H].r, 2 * kC * 4, bar);
-        };
-        if (ft == 0) {
-            fetch_v(0);
-            fetch_tp(0);
-        }
-        asm volatile("bar.sync 1, 64;" ::: "memory");
-        for (int c = 0; c < chunks && ok; ++c) {
-            ok = barrier_wait(smem_addr(&sm.tp_raw_full), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1));
-            if (!ok) break;
-            // ten blocks each of T and P, ten vectors a thread
-#pragma unroll
-            for (int i = 0; i < 10; ++i) {
-                const int x = ft + kSideThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
-                const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
-                const int row = 16 * bi + in / 16, col = 16 * bj + in % 16;
-                const uint32_t at = swizzled(2 * kC, row, col);
-                const float4 tv = *reinterpret_cast<const float4 *>(sm.tp_raw + 4 * x);
-                const float4 hi = make_float4(tf32_hi(tv.x), tf32_hi(tv.y), tf32_hi(tv.z), tf32_hi(tv.w));
-                *reinterpret_cast<float4 *>(sm.t + at) = hi;
-                *reinterpret_cast<float4 *>(sm.t + kC * 128 + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
-                *reinterpret_cast<float4 *>(sm.p + swizzled(kC, row, col)) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 13 || warp == 14) {
+            // ------------------------------------------------ T, P, and V, R and D of the chunks
+            const int ft = tid - kGroupThreads - kFeedThreads - 32;
+            for (int i = ft; i < kC * kC / 4; i += kSideThreads) {  // above the diagonal they stay zero
+                reinterpret_cast<uint4 *>(sm.t)[i] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4 *>(sm.t)[i + kC * kC / 4] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
             }
-            fence_async_smem();
-            barrier_arrive(smem_addr(&sm.tp_full));
-            asm volatile("bar.sync 1, 64;" ::: "memory");  // all have read what comes next over it
-            if (ft == 0 && c + 1 < chunks) {
-                fetch_tp(c + 1);
-                ok = barrier_wait(smem_addr(&sm.v_empty), c & 1);
-                if (ok) fetch_v(c + 1);
+            const auto fetch_tp = [&](int c) {
+                const uint32_t bar = smem_addr(&sm.tp_raw_full);
+                barrier_expect(bar, 2 * kTriangle * 4);
+                bulk_copy(smem_addr(sm.tp_raw), prep[static_cast<size_t>(c) * H].t, 2 * kTriangle * 4, bar);
+            };
+            const auto fetch_v = [&](int c) {
+                const uint32_t bar = smem_addr(&sm.v_full);
+                barrier_expect(bar, 2 * kC * 128 + 2 * kC * 4);
+                for (int half = 0; half < 2; ++half) tma_load3(smem_addr(sm.v[half]), &v_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
+                bulk_copy(smem_addr(&sm.rd[c & 1]), prep[static_cast<size_t>(c) * H].r, 2 * kC * 4, bar);
+            };
+            if (ft == 0) {
+                fetch_v(0);
+                fetch_tp(0);
             }
-        }
-    } else if (warp == 12) {
-        // ------------------------------------------------ products
-        constexpr uint32_t n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
-        const uint32_t kq = smem_addr(sm.kq), kt = smem_addr(sm.kt), tt = smem_addr(sm.t), p = smem_addr(sm.p);
-        // step s of 8 in an operand of blocks of 32 columns and `rows` rows
-        const auto step = [](uint32_t base, int rows, int s) { return tc_desc(base + (s >> 2) * rows * 128 + (s & 3) * 32, 16, 1024); };
-        for (int c = 0; c < chunks && ok; ++c) {
-            const uint32_t phase = c & 1;
-            ok = barrier_wait(smem_addr(&sm.kq_full), phase) && barrier_wait(smem_addr(&sm.x_full), phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
+            asm volatile("bar.sync 1, 64;" ::: "memory");
+            for (int c = 0; c < chunks && ok; ++c) {
+                ok = barrier_wait(smem_addr(&sm.tp_raw_full), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1));
+                if (!ok) break;
+                // ten blocks each of T and P, ten vectors a thread
 #pragma unroll
-                for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColK, tmem + kColHi + 8 * s, step(kq, 128, s), n128, s > 0);
+                for (int i = 0; i < 10; ++i) {
+                    const int x = ft + kSideThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
+                    const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
+                    const int row = 16 * bi + in / 16, col = 16 * bj + in % 16;
+                    const uint32_t at = swizzled(2 * kC, row, col);
+                    const float4 tv = *reinterpret_cast<const float4 *>(sm.tp_raw + 4 * x);
+                    const float4 hi = make_float4(tf32_hi(tv.x), tf32_hi(tv.y), tf32_hi(tv.z), tf32_hi(tv.w));
+                    *reinterpret_cast<float4 *>(sm.t + at) = hi;
+                    *reinterpret_cast<float4 *>(sm.t + kC * 128 + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
+                    *reinterpret_cast<float4 *>(sm.p + swizzled(kC, row, col)) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
+                }
+                fence_async_smem();
+                barrier_arrive(smem_addr(&sm.tp_full));
+                asm volatile("bar.sync 1, 64;" ::: "memory");  // all have read what comes next over it
+                if (ft == 0 && c + 1 < chunks) {
+                    fetch_tp(c + 1);
+                    ok = barrier_wait(smem_addr(&sm.v_empty), c & 1);
+                    if (ok) fetch_v(c + 1);
+                }
+            }
+        } else if (warp == 12) {
+            // ------------------------------------------------ products
+            constexpr uint32_t n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
+            const uint32_t kq = smem_addr(sm.kq), kt = smem_addr(sm.kt), tt = smem_addr(sm.t), p = smem_addr(sm.p);
+            // step s of 8 in an operand of blocks of 32 columns and `rows` rows
+            const auto step = [](uint32_t base, int rows, int s) { return tc_desc(base + (s >> 2) * rows * 128 + (s & 3) * 32, 16, 1024); };
+            for (int c = 0; c < chunks && ok; ++c) {
+                const uint32_t phase = c & 1;
+                // key rows 0-31 and 64-95 of X_0 come first
+                ok = barrier_wait(smem_addr(&sm.kq_full), phase);
 #pragma unroll
-                for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColK, tmem + kColLo + 8 * s, step(kq, 128, s), n64, true);
-                tc_commit(smem_addr(&sm.k_done));
-                tc_commit(smem_addr(&sm.kq_empty));
+                for (int b = 0; b < 2; ++b) {
+                    ok = ok && barrier_wait(smem_addr(&sm.x_full[b]), phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int s = 4 * b + (i >> 2) * 8 + (i & 3);
+                            tc_mma_tf32(tmem + kColK, tmem + kColHi + 8 * s, step(kq, 128, s), n128, b > 0 || i > 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int s = 4 * b + (i >> 2) * 8 + (i & 3);
+                            tc_mma_tf32(tmem + kColK, tmem + kColLo + 8 * s, step(kq, 128, s), n64, true);
+                        }
+                        if (b == 1) {
+                            tc_commit(smem_addr(&sm.k_done));
+                            tc_commit(smem_addr(&sm.kq_empty));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                ok = barrier_wait(smem_addr(&sm.tp_full), phase) && barrier_wait(smem_addr(&sm.r_full), phase);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 8 * s, step(tt, 128, s), n128, s > 0);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 64 + 8 * s, step(tt, 128, s), n64, true);
+                    tc_commit(smem_addr(&sm.u_done));
+                }
+                __syncwarp();
+                ok = barrier_wait(smem_addr(&sm.kt_full), phase) && barrier_wait(smem_addr(&sm.u_full), phase);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColX, tmem + kColHi + 8 * s, step(kt, 128, s & 7), n128, true);
+                    tc_commit(smem_addr(&sm.x_done));
+                    tc_commit(smem_addr(&sm.kt_empty));
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColY, tmem + kColK + 8 * s, step(p, 64, s), n64, true);
+                    tc_commit(smem_addr(&sm.y_done));
+                    tc_commit(smem_addr(&sm.tp_empty));
+                }
+                __syncwarp();
+            }
+            if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
+                barrier_init(smem_addr(&sm.item), 1);
+                tc_commit(smem_addr(&sm.item));
+                barrier_wait(smem_addr(&sm.item), 0);
             }
             __syncwarp();
-            ok = barrier_wait(smem_addr(&sm.tp_full), phase) && barrier_wait(smem_addr(&sm.r_full), phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 8 * s, step(tt, 128, s), n128, s > 0);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 64 + 8 * s, step(tt, 128, s), n64, true);
-                tc_commit(smem_addr(&sm.u_done));
-            }
-            __syncwarp();
-            ok = barrier_wait(smem_addr(&sm.kt_full), phase) && barrier_wait(smem_addr(&sm.u_full), phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColX, tmem + kColHi + 8 * s, step(kt, 128, s & 7), n128, true);
-                tc_commit(smem_addr(&sm.x_done));
-                tc_commit(smem_addr(&sm.kt_empty));
-#pragma unroll
-                for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColY, tmem + kColK + 8 * s, step(p, 64, s), n64, true);
-                tc_commit(smem_addr(&sm.y_done));
-                tc_commit(smem_addr(&sm.tp_empty));
-            }
-            __syncwarp();
         }
-        if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
-            barrier_init(smem_addr(&sm.item), 1);
-            tc_commit(smem_addr(&sm.item));
-            barrier_wait(smem_addr(&sm.item), 0);
-        }
-        __syncwarp();
     } else {
         // ------------------------------------------------ between the products: a lane is a column of the state
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupRegs));
         const int half = warp >> 2, j = (warp & 3) * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint8_t *v = sm.v[j >> 6] + (j & 7) * 2;
@@ -686,11 +717,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
             tmem_store32(base + kColHi + col, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
+            for (int i = 0; i < 32; i += 2) put_pair(w + i, minus(pair_at(x + i), pair_at(w + i)));
             tmem_store32(base + kColLo + col, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(x[i]) * x_next);
-            tmem_store32(base + kColX + col, w);
+            for (int i = 0; i < 32; i += 2) put_pair(x + i, __fmul2_rn(pair_at(x + i), make_float2(x_next, x_next)));
+            tmem_store32(base + kColX + col, x);
         };
         ok = barrier_wait(smem_addr(&sm.v_full), 0);
         ok = __all_sync(0xffffffffu, ok);
@@ -703,10 +734,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = fresh ? 0u : __float_as_uint(state[static_cast<size_t>(col + i) * kD + j]);
                 put(col, x, x_next);
+                tmem_wait_store();
+                tc_fence_before();
+                barrier_arrive(smem_addr(&sm.x_full[b]));
             }
-            tmem_wait_store();
-            tc_fence_before();
-            barrier_arrive(smem_addr(&sm.x_full));
         }
         uint32_t ys[16];  // the last chunk's Y, two tokens a register, until there is time to store it
         const auto store_y = [&](int c) {
@@ -748,7 +779,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tmem_load32(base + kColK + 32 * half, x);
             tmem_wait_load();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) vs[i] = fmaf(-rd.r[32 * half + i], __uint_as_float(x[i]), vs[i]);
+            for (int i = 0; i < 32; i += 2) {
+                const float2 r = *reinterpret_cast<const float2 *>(&rd.r[32 * half + i]);
+                const float2 y = __ffma2_rn(make_float2(-r.x, -r.y), pair_at(x + i), make_float2(vs[i], vs[i + 1]));
+                vs[i] = y.x;
+                vs[i + 1] = y.y;
+            }
             if (left < 32) {  // rows behind the prompt's last are not its own
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -758,12 +794,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_cut(vs[i]));
             tmem_store32(base + kColLo + 32 * half, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(vs[i] - __uint_as_float(w[i]));
+            for (int i = 0; i < 32; i += 2) put_pair(x + i, minus(make_float2(vs[i], vs[i + 1]), pair_at(w + i)));
             tmem_store32(base + kColLo + 64 + 32 * half, x);
             tmem_wait_store();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.r_full));
-            if (c > 0) store_y(c - 1);
             // U, and D U
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.u_done), phase));
             if (!ok) break;
@@ -772,23 +807,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tmem_load32(base + kColHi + 64 + 32 * half, w);
             tmem_wait_load();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(w[i]));
-                w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
-            }
+            for (int i = 0; i < 32; i += 2) put_pair(x + i, __fadd2_rn(pair_at(x + i), pair_at(w + i)));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
             tmem_store32(base + kColK + 32 * half, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                x[i] = __float_as_uint(rd.d[32 * half + i] * __uint_as_float(x[i]));
-                w[i] = __float_as_uint(tf32_cut(__uint_as_float(x[i])));
-            }
+            for (int i = 0; i < 32; i += 2) put_pair(x + i, __fmul2_rn(pair_at(x + i), *reinterpret_cast<const float2 *>(&rd.d[32 * half + i])));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_cut(__uint_as_float(x[i])));
             tmem_store32(base + kColHi + 32 * half, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(w[i]));
+            for (int i = 0; i < 32; i += 2) put_pair(x + i, minus(pair_at(x + i), pair_at(w + i)));
             tmem_store32(base + kColHi + 64 + 32 * half, x);
             tmem_wait_store();
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.u_full));
+            if (c > 0) store_y(c - 1);
             // the state after the chunk
             float x_next = 0.0f;
             if (c + 1 < chunks) {
@@ -799,8 +833,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.x_done), phase));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
+            // the first half of this thread's rows, then Y (whose products come behind the state's; the next chunk's
+            // go where it is), and those products may begin
+            const auto update = [&](int b) {
                 const int col = 64 * half + 32 * b;
                 tmem_load32(base + kColX + col, x);
                 tmem_wait_load();
@@ -810,8 +845,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 32; ++i) state[static_cast<size_t>(col + i) * kD + j] = __uint_as_float(x[i]);
                 }
-            }
-            // Y, whose products come behind the state's; the next chunk's go where it is
+            };
+            update(0);
             ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.y_done), phase));
             if (!ok) break;
             tc_fence_after();
@@ -819,10 +854,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tmem_wait_load();
             tmem_wait_store();
             tc_fence_before();
-            barrier_arrive(smem_addr(&sm.x_full));
+            barrier_arrive(smem_addr(&sm.x_full[0]));
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 ys[i] = narrow1<BF16>(__uint_as_float(x[2 * i])) | static_cast<uint32_t>(narrow1<BF16>(__uint_as_float(x[2 * i + 1]))) << 16;
+            update(1);
+            tmem_wait_store();
+            tc_fence_before();
+            barrier_arrive(smem_addr(&sm.x_full[1]));
         }
         if (ok) store_y(chunks - 1);
     }
