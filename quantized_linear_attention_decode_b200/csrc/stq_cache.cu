@@ -98,9 +98,10 @@ __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long lon
         if ((lane & 3) == 0) atomicOr(c.err, kErrNonFinite);
     }
     int z[8];
+    const float inv = __frcp_rn(sf);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float y = sf > 0.0f ? rintf(__fdiv_rn(x[j], sf)) : 0.0f;
+        const float y = sf > 0.0f ? rounded_quotient(x[j], sf, inv) : 0.0f;
         z[j] = static_cast<int>(fminf(fmaxf(y, -7.0f), 7.0f));
     }
     const int o = static_cast<int>(at & (kHalf - 1)), g = l >> 2, t = l & 3;

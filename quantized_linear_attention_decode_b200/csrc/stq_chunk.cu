@@ -13,8 +13,8 @@
 // Precision.  The state has to come out as the recurrence in fp32 gives it.  k is a
 // 16-bit value, exact in tf32 (11 bits); X_0, V - K X_0, T and D U are fp32 values
 // and enter the tensor core as two tf32 terms, x = hi + lo, 2^-21 of x left: 2 products
-// against k, 3 of the 4 for T times a vector.  Y is rounded to 16 bits and takes one
-// term of each (rounded to nearest, 2^-11).  Sums are fp32.
+// against k, 3 of the 4 for T times a vector.  Y is rounded to 16 bits: of R Q, P and U one
+// term each, rounded to nearest (2^-11).  Sums are fp32.
 #include <cmath>
 
 #include "stq_host.h"
@@ -365,10 +365,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
 //   256  X_0^T lo; then (V - R K X_0)^T hi | lo
 //   384  (K X_0)^T; then U^T hi
 //   448  (diag(R) Q X_0)^T, then Y^T
-// A product of 8 deep takes 64 cycles whatever its width up to 128 columns, for its A
-// operand's sake, so K and Q stand under each other for the hi term, and T's two terms for
-// theirs: 16 x 128 and 16 x 64 for K and Q, 8 x 128 and 8 x 64 for T, 16 x 128 for the update,
-// 8 x 64 for Y's, 4600 cycles.  Bound by the chain of all but Y's with what stands
+// A product of 8 deep takes about 64 cycles at 128 columns and 45 at 64, for its A operand's
+// sake, so K and Q stand under each other for the hi term, and T's two terms for R's.  Bound by the chain of all but Y's with what stands
 // between them.
 
 constexpr int kGroupThreads = 256;  // warps 0-7: two for each quarter of the lanes, half of the columns each

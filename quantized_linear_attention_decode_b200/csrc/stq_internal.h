@@ -123,6 +123,15 @@ constexpr int kPreparedBytes = 20992;
 constexpr long long prompt_chunks(int n, int total) { return static_cast<long long>(total) / kPromptChunk + n; }  // at most
 cudaError_t launch_prompt_chunks(const PoolView &p, const PromptIO &io, cudaStream_t stream);
 
+// rint(fl(x / s)) for a scale s > 0 and |x / s| below 2^7 or so: a product with the reciprocal is within 2^-15 of
+// the quotient, which decides unless it lies that near a tie; the division is made only there.
+__device__ __forceinline__ float rounded_quotient(float x, float s, float inv)
+{
+    const float q = x * inv, z = rintf(q);
+    // (also where the reciprocal of a subnormal scale overflows: the comparison fails)
+    return fabsf(fabsf(q - z) - 0.5f) >= 1e-4f ? z : rintf(__fdiv_rn(x, s));
+}
+
 void count_launch();
 
 // Records a printf-style message for stq_last_error() and returns st.

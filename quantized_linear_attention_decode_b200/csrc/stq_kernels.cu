@@ -118,11 +118,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
         if (p.scale_bytes == 2) s = __half2float(s16);  // the scale as stored
         bad |= !isfinite(s);
         uint32_t code[4];
+        const float inv = __frcp_rn(s);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             int zz = 0;
             if (s > 0.0f && isfinite(s)) {
-                float rz = rintf(__fdiv_rn(mu[t], s));
+                float rz = rounded_quotient(mu[t], s, inv);
                 rz = fminf(fmaxf(rz, -static_cast<float>(qb)), static_cast<float>(qb));
                 zz = static_cast<int>(rz);
             }

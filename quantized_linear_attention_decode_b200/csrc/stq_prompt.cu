@@ -38,53 +38,86 @@ template <int RP>
 struct __align__(16) Staged {
     float k[kTokens][kD], q[kTokens][kD];
     float v[kTokens][kCtaCols<RP>];
-    float a[kTokens], b[kTokens], kq[kTokens];
+    // before the token X~ is multiplied by `rescale` (1: left alone); then X = c X~ with its decay, and 1 / c
+    float4 scale[kTokens];  // rescale, c, 1 / c, gate
+    float kq[kTokens];
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// The head's rows of tokens [t0, t0 + m) into shared memory, as fp32; tokens behind them as zeros.
+// The head's rows of tokens [t0, t0 + m), as they come (zeros behind them), in the registers of all threads...
 template <int RP>
-__device__ __forceinline__ void stage(Staged<RP> &s, const PromptIO &io, int H, int h, int col0, long long t0, int m)
-{
-    const int tid = threadIdx.x;
-    for (int e = tid; e < kTokens * kD / 8; e += kThreads) {
-        const int t = e / (kD / 8), d = e % (kD / 8) * 8;
-        float x[8], z[8];
+struct Incoming {
+    static constexpr int kVec = kTokens * kD / 8 / kThreads, kVecV = (kTokens * kCtaCols<RP> / 8 + kThreads - 1) / kThreads;
+    float k[kVec][8], q[kVec][8], v[kVecV][8], a, b;
+
+    __device__ __forceinline__ void load(const PromptIO &io, int H, int h, int col0, long long t0, int m)
+    {
+        const int tid = threadIdx.x;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = z[j] = 0.0f;
-        if (t < m) {
-            load8(io.k.data, (t0 + t) * io.k.token_stride + h * io.k.head_stride + d, io.dtype, x);
-            load8(io.q.data, (t0 + t) * io.q.token_stride + h * io.q.head_stride + d, io.dtype, z);
+        for (int i = 0; i < kVec; ++i) {
+            const int t = (tid + i * kThreads) / (kD / 8), d = tid % (kD / 8) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) k[i][j] = q[i][j] = 0.0f;
+            if (t < m) {
+                load8(io.k.data, (t0 + t) * io.k.token_stride + h * io.k.head_stride + d, io.dtype, k[i]);
+                load8(io.q.data, (t0 + t) * io.q.token_stride + h * io.q.head_stride + d, io.dtype, q[i]);
+            }
         }
-        *reinterpret_cast<float4 *>(&s.k[t][d]) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(&s.k[t][d + 4]) = make_float4(x[4], x[5], x[6], x[7]);
-        *reinterpret_cast<float4 *>(&s.q[t][d]) = make_float4(z[0], z[1], z[2], z[3]);
-        *reinterpret_cast<float4 *>(&s.q[t][d + 4]) = make_float4(z[4], z[5], z[6], z[7]);
-        float kq = 0.0f;  // 16 lanes hold a token
 #pragma unroll
-        for (int j = 0; j < 8; ++j) kq = fmaf(x[j], z[j], kq);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
-        if (tid % 16 == 0) s.kq[t] = kq;
+        for (int i = 0; i < kVecV; ++i) {
+            const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 8), d = e % (kCtaCols<RP> / 8) * 8;
+            if (t < m) load8(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, io.dtype, v[i]);
+        }
+        a = tid < m ? io.alpha[(t0 + tid) * H + h] : 1.0f;
+        b = tid < m ? io.beta[(t0 + tid) * H + h] : 0.0f;
     }
-    for (int e = tid; e < kTokens * kCtaCols<RP> / 8; e += kThreads) {
-        const int t = e / (kCtaCols<RP> / 8), d = e % (kCtaCols<RP> / 8) * 8;
-        if (t < m) {
-            float x[8];
-            load8(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, io.dtype, x);
-            *reinterpret_cast<float4 *>(&s.v[t][d]) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(&s.v[t][d + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+
+    // ... and from there to shared memory.  c: the product of decays that X~ stands under, kept by the first warp.
+    __device__ __forceinline__ void store(Staged<RP> &s, int m, float &c) const
+    {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int t = (tid + i * kThreads) / (kD / 8), d = tid % (kD / 8) * 8;
+            *reinterpret_cast<float4 *>(&s.k[t][d]) = make_float4(k[i][0], k[i][1], k[i][2], k[i][3]);
+            *reinterpret_cast<float4 *>(&s.k[t][d + 4]) = make_float4(k[i][4], k[i][5], k[i][6], k[i][7]);
+            *reinterpret_cast<float4 *>(&s.q[t][d]) = make_float4(q[i][0], q[i][1], q[i][2], q[i][3]);
+            *reinterpret_cast<float4 *>(&s.q[t][d + 4]) = make_float4(q[i][4], q[i][5], q[i][6], q[i][7]);
+            float kq = 0.0f;  // 16 lanes hold a token
+#pragma unroll
+            for (int j = 0; j < 8; ++j) kq = fmaf(k[i][j], q[i][j], kq);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
+            if (tid % 16 == 0) s.kq[t] = kq;
+        }
+#pragma unroll
+        for (int i = 0; i < kVecV; ++i) {
+            const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 8), d = e % (kCtaCols<RP> / 8) * 8;
+            if (t < m) {
+                *reinterpret_cast<float4 *>(&s.v[t][d]) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                *reinterpret_cast<float4 *>(&s.v[t][d + 4]) = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+            }
+        }
+        if (tid < 32) {
+            float rescale = 1.0f, mine = 1.0f;
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                const float next = c * __shfl_sync(0xffffffffu, a, t);
+                const bool out = !(fabsf(next) >= 0x1p-20f && fabsf(next) <= 0x1p20f);
+                if (tid == t) {
+                    rescale = out ? next : 1.0f;
+                    mine = out ? 1.0f : next;
+                }
+                c = out ? 1.0f : next;
+            }
+            if (tid < kTokens) s.scale[tid] = make_float4(rescale, mine, 1.0f / mine, b);
         }
     }
-    if (tid < m) {
-        s.a[tid] = io.alpha[(t0 + tid) * H + h];
-        s.b[tid] = io.beta[(t0 + tid) * H + h];
-    }
-}
+};
 
 template <int RP>
-__global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : 4) prompt_tokens_kernel(PoolView p, PromptIO io)
+__global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : RP == 8 ? 3 : 4) prompt_tokens_kernel(PoolView p, PromptIO io)
 {
     extern __shared__ __align__(16) uint8_t raw_smem[];
     Staged<RP> *st = reinterpret_cast<Staged<RP> *>(raw_smem);  // two of them
@@ -126,12 +159,15 @@ __global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : 4) prompt_tokens_kerne
             x[b][3][i] = make_float2(w[2 * i].w, w[2 * i + 1].w);
         }
     }
-    float c = 1.0f;  // X = c x
-    stage<RP>(st[0], io, p.H, h, col0, first, min(len, kTokens));
+    float c = 1.0f, last = 1.0f;  // X = last x; c runs ahead in the first warp
+    Incoming<RP> in;
+    in.load(io, p.H, h, col0, first, min(len, kTokens));
+    in.store(st[0], min(len, kTokens), c);
     __syncthreads();
     for (int t0 = 0; t0 < len; t0 += kTokens) {
         const Staged<RP> &s = st[t0 / kTokens & 1];
-        if (t0 + kTokens < len) stage<RP>(st[(t0 / kTokens & 1) ^ 1], io, p.H, h, col0, first + t0 + kTokens, min(len - t0 - kTokens, kTokens));
+        const int coming = min(len - t0 - kTokens, kTokens);  // tokens after these
+        if (coming > 0) in.load(io, p.H, h, col0, first + t0 + kTokens, coming);
         const int m = min(len - t0, kTokens);
         for (int t = 0; t < m; ++t) {
             float2 sk[kCols], sq[kCols];
@@ -150,44 +186,54 @@ __global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : 4) prompt_tokens_kerne
                     sq[j] = fma2(x[b][j][1], make_float2(q4.z, q4.w), sq[j]);
                 }
             }
-            float vk[kCols], vq[kCols];
+            const float4 scale = s.scale[t];
+            const float kq = s.kq[t];
+            // the sums over the lanes of a column: each exchange halves the columns that a lane is left with, until
+            // lane r has column r mod 4's two
+            float vk, vq;
+            const float v = s.v[t][col + (r & 3)];
+            {
+                const bool odd = r & 1, two = r & 2;
+                float k2[2], q2[2];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                vk[j] = sk[j].x + sk[j].y;
-                vq[j] = sq[j].x + sq[j].y;
+                for (int j = 0; j < 2; ++j) {
+                    const float ke = sk[2 * j].x + sk[2 * j].y, ko = sk[2 * j + 1].x + sk[2 * j + 1].y;
+                    const float qe = sq[2 * j].x + sq[2 * j].y, qo = sq[2 * j + 1].x + sq[2 * j + 1].y;
+                    k2[j] = (odd ? ko : ke) + __shfl_xor_sync(0xffffffffu, odd ? ke : ko, 1);
+                    q2[j] = (odd ? qo : qe) + __shfl_xor_sync(0xffffffffu, odd ? qe : qo, 1);
+                }
+                vk = (two ? k2[1] : k2[0]) + __shfl_xor_sync(0xffffffffu, two ? k2[0] : k2[1], 2);
+                vq = (two ? q2[1] : q2[0]) + __shfl_xor_sync(0xffffffffu, two ? q2[0] : q2[1], 2);
             }
 #pragma unroll
-            for (int o = RP / 2; o > 0; o >>= 1)
-#pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    vk[j] += __shfl_xor_sync(0xffffffffu, vk[j], o);
-                    vq[j] += __shfl_xor_sync(0xffffffffu, vq[j], o);
-                }
-            const float a = s.a[t], beta = s.b[t], kq = s.kq[t];
-            c *= a;
-            if (!(fabsf(c) >= 0x1p-20f && fabsf(c) <= 0x1p20f)) {  // the same for every thread of the head
+            for (int o = 4; o < RP; o *= 2) {
+                vk += __shfl_xor_sync(0xffffffffu, vk, o);
+                vq += __shfl_xor_sync(0xffffffffu, vq, o);
+            }
+            if (scale.x != 1.0f) {  // the same for every thread of the head
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                     for (int j = 0; j < kCols; ++j)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) x[b][j][i] = make_float2(x[b][j][i].x * c, x[b][j][i].y * c);
-#pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    vk[j] *= c;
-                    vq[j] *= c;
-                }
-                c = 1.0f;
+                        for (int i = 0; i < 2; ++i) x[b][j][i] = make_float2(x[b][j][i].x * scale.x, x[b][j][i].y * scale.x);
+                vk *= scale.x;
+                vq *= scale.x;
             }
-            const float inv = __frcp_rn(c);
-            const float4 v4 = *reinterpret_cast<const float4 *>(&s.v[t][col]);
-            const float v[kCols] = {v4.x, v4.y, v4.z, v4.w};
-            float u[kCols], y[kCols];
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                u[j] = beta * fmaf(-c, vk[j], v[j]);
-                y[j] = fmaf(c, vq[j], u[j] * kq);
-                u[j] *= inv;
+            last = scale.y;
+            float own = scale.w * fmaf(-scale.y, vk, v);
+            const float y = fmaf(scale.y, vq, own * kq);
+            own *= scale.z;
+            float u[kCols];
+            {
+                const bool odd = r & 1, two = r & 2;
+                const float beside = __shfl_xor_sync(0xffffffffu, own, 1);
+                const float even = odd ? beside : own, uneven = odd ? own : beside;
+                const float even2 = __shfl_xor_sync(0xffffffffu, even, 2), uneven2 = __shfl_xor_sync(0xffffffffu, uneven, 2);
+                u[0] = two ? even2 : even;
+                u[1] = two ? uneven2 : uneven;
+                u[2] = two ? even : even2;
+                u[3] = two ? uneven : uneven2;
             }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
@@ -197,23 +243,9 @@ __global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : 4) prompt_tokens_kerne
                     x[b][j][0] = fma2(make_float2(k4[b].x, k4[b].y), uu, x[b][j][0]);
                     x[b][j][1] = fma2(make_float2(k4[b].z, k4[b].w), uu, x[b][j][1]);
                 }
-            if (r == 0) {
-                const int64_t at = ((first + t0 + t) * p.H + h) * kD + col0 + col;
-                if (io.dtype == STQ_F32) {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(io.y) + at) = make_float4(y[0], y[1], y[2], y[3]);
-                } else {
-                    uint2 w;
-                    if (io.dtype == STQ_BF16) {
-                        const __nv_bfloat162 lo = __floats2bfloat162_rn(y[0], y[1]), hi = __floats2bfloat162_rn(y[2], y[3]);
-                        w = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-                    } else {
-                        const __half2 lo = __floats2half2_rn(y[0], y[1]), hi = __floats2half2_rn(y[2], y[3]);
-                        w = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-                    }
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(io.y) + at) = w;
-                }
-            }
+            if (r < 4) store_from_float(io.y, ((first + t0 + t) * p.H + h) * kD + col0 + col + r, io.dtype, y);
         }
+        if (coming > 0) in.store(st[(t0 / kTokens & 1) ^ 1], coming, c);
         __syncthreads();
     }
 #pragma unroll
@@ -221,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : 4) prompt_tokens_kerne
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float *to = S + static_cast<size_t>(4 * (r + RP * b) + 2 * i) * kD;
-            *reinterpret_cast<float4 *>(to) = make_float4(c * x[b][0][i].x, c * x[b][1][i].x, c * x[b][2][i].x, c * x[b][3][i].x);
-            *reinterpret_cast<float4 *>(to + kD) = make_float4(c * x[b][0][i].y, c * x[b][1][i].y, c * x[b][2][i].y, c * x[b][3][i].y);
+            *reinterpret_cast<float4 *>(to) = make_float4(last * x[b][0][i].x, last * x[b][1][i].x, last * x[b][2][i].x, last * x[b][3][i].x);
+            *reinterpret_cast<float4 *>(to + kD) = make_float4(last * x[b][0][i].y, last * x[b][1][i].y, last * x[b][2][i].y, last * x[b][3][i].y);
         }
 }
 
@@ -249,6 +281,8 @@ cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t st
         rows_mappable(io.k, p.H, total) && rows_mappable(io.v, p.H, total))
         return launch_prompt_chunks(p, io, stream);
     const long long units = static_cast<long long>(io.n) * p.H;
+    // more lanes a column shorten a token (16: 880 cycles at three warps on a scheduler) and cost a fixed part of
+    // each warp's instructions; enough warps to fill the schedulers once decide
     if (units >= 256) return launch_tokens<4>(p, io, stream);
     return units >= 128 ? launch_tokens<8>(p, io, stream) : launch_tokens<16>(p, io, stream);
 }

@@ -425,56 +425,74 @@ def stq_last_error() -> str:
 # ------------------------------------------------------------------ prompts and the 4-bit cache
 
 
+_KINDS = {}  # torch dtype -> stq_dtype, filled on first use (torch is imported with the first tensor)
+
+
 def _dtype(t, name="tensor"):
     import torch
-    kinds = {torch.bfloat16: STQ_BF16, torch.float16: STQ_F16, torch.float32: STQ_F32}
-    if not isinstance(t, torch.Tensor) or t.dtype not in kinds:
+    if not _KINDS:
+        _KINDS.update({torch.bfloat16: STQ_BF16, torch.float16: STQ_F16, torch.float32: STQ_F32})
+    kind = _KINDS.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if kind is None:
         raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
-    return kinds[t.dtype]
+    return kind
 
 
-def _rows(t, like, shape, name):
-    """A [tokens, heads, 128] tensor of any token and head strides as a stq_rows."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda or t.device != like.device:
+def _rows(t, dtype, index, shape, name):
+    """A [tokens, heads, 128] tensor of any token and head strides on device `index` as a stq_rows."""
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on the CUDA device of the other tensors")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.numel() > 0 and t.stride(2) != 1:
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.numel() > 0:
         raise ValueError(f"{name}: the 128 values of a head must be contiguous")
     # a stride over one element is never taken
-    return _Rows(t.data_ptr(), t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0)
+    return _Rows(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0)
 
 
-def _on(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device} in one call")
+def _flat(t, dtype, index, shape, name):
+    """The address of a contiguous tensor on device `index`."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the CUDA device of the other tensors")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _stream_of(stream, device):
+def _stream_of(stream, index):
+    """The cudaStream_t of `stream` (a torch stream or an address), or of the device's current one."""
     import torch
-    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without the stream object that nobody keeps
+        return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _scratch(workspace, nbytes, device, stream):
-    """The caller's workspace, or one from torch's allocator for the stream that the call runs on."""
+def _scratch(workspace, nbytes, index, stream):
+    """Address and bytes of the caller's workspace, or of one from torch's allocator for the stream that the call runs
+    on (returned too: it has to live until the call has been made)."""
     import torch
     if workspace is None:
+        device = torch.device("cuda", index)
         if stream is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         else:
             s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
             with torch.cuda.stream(s):
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return workspace, nbytes
+        return workspace.data_ptr(), nbytes, workspace
+    if workspace.get_device() != index:
+        raise ValueError("workspace must be on the CUDA device of the other tensors")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def stq_prompt_workspace(pool: Pool, n: int, total: int) -> int:
@@ -493,19 +511,17 @@ def stq_prompt_step(pool: Pool, req_idx, slot_idx, seq_start, q, k, v, beta, alp
     import torch
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [total, H, 128] tensor")
-    n, r, s = _idx(pool, req_idx, slot_idx)
-    total, device = int(q.shape[0]), pool.device
-    shape = (total, pool.H, 128)
-    _on(device, req_idx, slot_idx, seq_start, q, k, v, beta, alpha, y, state, fresh, workspace)
-    qr, kr, vr = (_rows(t, q, shape, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
-    f = torch.float32
-    work, nbytes = _scratch(workspace, stq_prompt_workspace(pool, n, total), device, stream)
+    n, total, dev, dt, i32, f = req_idx.numel(), q.shape[0], pool.device.index, q.dtype, torch.int32, torch.float32
+    kind, shape = _dtype(q, "q"), (total, pool.H, 128)
+    qr, kr, vr = (_rows(t, dt, dev, shape, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    work, nbytes, keep = _scratch(workspace, 0 if workspace is not None else stq_prompt_workspace(pool, n, total), dev, stream)
     _check(load().stq_prompt_step(
-        pool.handle, r, s, n, _dev(seq_start, torch.int32, (n + 1,), "seq_start"), total,
-        None if fresh is None else _dev(fresh, torch.int32, (n,), "fresh"), _dtype(q, "q"), C.byref(qr), C.byref(kr),
-        C.byref(vr), _dev(beta, f, (total, pool.H), "beta"), _dev(alpha, f, (total, pool.H), "alpha"),
-        _dev(y, q.dtype, shape, "y"), _dev(state, f, (n, pool.H, 128, 128), "state"), C.c_void_p(work.data_ptr()), nbytes,
-        _stream_of(stream, device)))
+        pool.handle, _flat(req_idx, i32, dev, (n,), "req_idx"), _flat(slot_idx, i32, dev, (n,), "slot_idx"), n,
+        _flat(seq_start, i32, dev, (n + 1,), "seq_start"), total,
+        None if fresh is None else _flat(fresh, i32, dev, (n,), "fresh"), kind, C.byref(qr), C.byref(kr), C.byref(vr),
+        _flat(beta, f, dev, (total, pool.H), "beta"), _flat(alpha, f, dev, (total, pool.H), "alpha"),
+        _flat(y, dt, dev, shape, "y"), _flat(state, f, dev, (n, pool.H, 128, 128), "state"), work, nbytes,
+        _stream_of(stream, dev)))
 
 
 def stq_attn_prompt(q_start, k_start, q, k, v, y, scale=None, err=None, stream=None) -> None:
@@ -516,19 +532,20 @@ def stq_attn_prompt(q_start, k_start, q, k, v, y, scale=None, err=None, stream=N
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise ValueError(f"{name} must be a [tokens, heads, 128] tensor")
-    n = int(q_start.numel()) - 1
+    n = q_start.numel() - 1
     if n < 0:
         raise ValueError("q_start must have n + 1 entries")
-    device = q.device
-    _on(device, q_start, k_start, k, v, y, err)
-    tq, heads, tk, kv = int(q.shape[0]), int(q.shape[1]), int(k.shape[0]), int(k.shape[1])
-    qr, kr, vr = _rows(q, q, (tq, heads, 128), "q"), _rows(k, q, (tk, kv, 128), "k"), _rows(v, q, (tk, kv, 128), "v")
-    i32 = torch.int32
+    if not q.is_cuda:
+        raise ValueError("q must be on a CUDA device")
+    (tq, heads, _), (tk, kv, _), dev, dt, i32 = q.shape, k.shape, q.get_device(), q.dtype, torch.int32
+    kind = _dtype(q, "q")
+    qr, kr, vr = (_rows(t, dt, dev, shape, name) for t, shape, name in
+                  ((q, (tq, heads, 128), "q"), (k, (tk, kv, 128), "k"), (v, (tk, kv, 128), "v")))
     _check(load().stq_attn_prompt(
-        _dev(q_start, i32, (n + 1,), "q_start"), _dev(k_start, i32, (n + 1,), "k_start"), n, heads, kv, tq, tk,
-        _dtype(q, "q"), C.byref(qr), C.byref(kr), C.byref(vr), 128 ** -0.5 if scale is None else float(scale),
-        _dev(y, q.dtype, (tq, heads, 128), "y"), None if err is None else _dev(err, i32, (1,), "err"),
-        _stream_of(stream, device)))
+        _flat(q_start, i32, dev, (n + 1,), "q_start"), _flat(k_start, i32, dev, (n + 1,), "k_start"), n, heads, kv, tq, tk,
+        kind, C.byref(qr), C.byref(kr), C.byref(vr), 128 ** -0.5 if scale is None else float(scale),
+        _flat(y, dt, dev, (tq, heads, 128), "y"), None if err is None else _flat(err, i32, dev, (1,), "err"),
+        _stream_of(stream, dev)))
 
 
 class Cache:
@@ -572,23 +589,21 @@ def stq_cache_append(cache: Cache, slot, k, v, stream=None) -> None:
     """Quantize the tokens k, v [n, num_kv_heads, 128] into the token slots slot (int64 [n], page * 64 + offset;
     negative ones are skipped)."""
     import torch
-    n = int(slot.numel())
-    shape = (n, cache.num_kv_heads, 128)
-    _on(cache.device, slot, k, v)
-    kr, vr = _rows(k, k, shape, "k"), _rows(v, k, shape, "v")
-    _check(load().stq_cache_append(cache.handle, _dev(slot, torch.int64, (n,), "slot"), n, _dtype(k, "k"), C.byref(kr),
-                                   C.byref(vr), _stream_of(stream, cache.device)))
+    n, dev = slot.numel(), cache.device.index
+    kind, shape = _dtype(k, "k"), (n, cache.num_kv_heads, 128)
+    kr, vr = _rows(k, k.dtype, dev, shape, "k"), _rows(v, k.dtype, dev, shape, "v")
+    _check(load().stq_cache_append(cache.handle, _flat(slot, torch.int64, dev, (n,), "slot"), n, kind, C.byref(kr),
+                                   C.byref(vr), _stream_of(stream, dev)))
 
 
 def stq_cache_read(cache: Cache, slot, k_out, v_out, stream=None) -> None:
     """The fp32 values that the cache stands for at the token slots, into k_out and v_out [n, num_kv_heads, 128]."""
     import torch
-    n = int(slot.numel())
+    n, dev, f = slot.numel(), cache.device.index, torch.float32
     shape = (n, cache.num_kv_heads, 128)
-    _on(cache.device, slot, k_out, v_out)
-    _check(load().stq_cache_read(cache.handle, _dev(slot, torch.int64, (n,), "slot"), n,
-                                 _dev(k_out, torch.float32, shape, "k_out"), _dev(v_out, torch.float32, shape, "v_out"),
-                                 _stream_of(stream, cache.device)))
+    _check(load().stq_cache_read(cache.handle, _flat(slot, torch.int64, dev, (n,), "slot"), n,
+                                 _flat(k_out, f, dev, shape, "k_out"), _flat(v_out, f, dev, shape, "v_out"),
+                                 _stream_of(stream, dev)))
 
 
 def stq_attn_decode_workspace(cache: Cache, n: int, num_heads: int) -> int:
@@ -602,23 +617,20 @@ def stq_attn_decode(cache: Cache, page_table, seq_len, q, y, scale=None, workspa
     """Attention of one query token a sequence over the cache: page_table int32 [n, max_pages], seq_len int32 [n],
     q and y [n, num_heads, 128]; scale defaults to 1 / sqrt(128)."""
     import torch
-    n = int(seq_len.numel())
     if page_table.dim() != 2 or q.dim() != 3:
         raise ValueError("page_table must be [n, max_pages] and q [n, num_heads, 128]")
-    heads = int(q.shape[1])
-    shape = (n, heads, 128)
-    _on(cache.device, page_table, seq_len, q, y, workspace)
-    qr = _rows(q, q, shape, "q")
-    work, nbytes = _scratch(workspace, stq_attn_decode_workspace(cache, n, heads), cache.device, stream)
+    n, pages, heads, dev, dt, i32 = seq_len.numel(), page_table.shape[1], q.shape[1], cache.device.index, q.dtype, torch.int32
+    kind, shape = _dtype(q, "q"), (n, heads, 128)
+    qr = _rows(q, dt, dev, shape, "q")
+    work, nbytes, keep = _scratch(workspace, 0 if workspace is not None else stq_attn_decode_workspace(cache, n, heads), dev, stream)
     _check(load().stq_attn_decode(
-        cache.handle, _dev(page_table, torch.int32, (n, page_table.shape[1]), "page_table"), int(page_table.shape[1]),
-        _dev(seq_len, torch.int32, (n,), "seq_len"), n, heads, _dtype(q, "q"), C.byref(qr),
-        128 ** -0.5 if scale is None else float(scale), _dev(y, q.dtype, shape, "y"), C.c_void_p(work.data_ptr()), nbytes,
-        _stream_of(stream, cache.device)))
+        cache.handle, _flat(page_table, i32, dev, (n, pages), "page_table"), pages, _flat(seq_len, i32, dev, (n,), "seq_len"),
+        n, heads, kind, C.byref(qr), 128 ** -0.5 if scale is None else float(scale), _flat(y, dt, dev, shape, "y"), work,
+        nbytes, _stream_of(stream, dev)))
 
 
 def stq_cache_check(cache: Cache, stream=None, raise_on_error: bool = True) -> int:
-    st = load().stq_cache_check(cache.handle, _stream_of(stream, cache.device))
+    st = load().stq_cache_check(cache.handle, _stream_of(stream, cache.device.index))
     if raise_on_error:
         _check(st)
     return st
