@@ -179,9 +179,8 @@ __global__ void __launch_bounds__(256) read_kernel(CacheView c, const long long 
 // largest weight.  Sums are fp32.
 
 constexpr int kWarps = 4;   // of a CTA; they share nothing but its memory
-constexpr int kUnit = 2;     // halves of a unit
 constexpr int kStagesW = 2;  // units in a warp's ring
-constexpr int kUnitTokens = kUnit * kHalf, kUnitBytes = kUnit * kHalfBlock;
+constexpr int kUnitBytes = STQ_CACHE_BLOCK;  // a page of a head; quarters of one take a half
 
 constexpr float kSlack = 4.0f;           // how far a score may lie above R
 
@@ -237,7 +236,7 @@ __device__ __forceinline__ Shares shares_of(const AttnArgs &a)
     Shares s;
     s.subs = a.c.heads * a.blocks;
     s.units = pages_before(a, a.n) * s.subs;
-    s.shift = s.units * 4 <= a.warps ? 2 : kUnit == 1 ? 1 : 0;
+    s.shift = s.units * 4 <= a.warps ? 2 : 0;
     s.units <<= s.shift;
     s.warps = static_cast<int>(min(static_cast<long long>(a.warps), max(s.units, 1ll)));
     s.q = s.units / s.warps;
@@ -317,7 +316,7 @@ __device__ __forceinline__ int feed_next(const AttnArgs &a, const Shares &s, Fee
     }
     const int id = __shfl_sync(0xffffffffu, f.ids, f.w.unit - f.first);
     *head = f.w.sub / a.blocks;
-    *half = s.shift == 2 ? f.w.unit >> 1 & 1 : kUnit == 1 ? f.w.unit & 1 : 0;
+    *half = s.shift == 2 ? f.w.unit >> 1 & 1 : 0;
     ++f.w.unit;
     --f.left;
     return id < 0 || id >= a.c.pages ? -2 : id;
@@ -677,8 +676,8 @@ __global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel
                 const uint8_t *page = sm.stage[warp][k];
                 if (s.shift == 2) {
                     if (u * 16 < len) take_unit<NT, 1>(sg, page, len - (u >> 1) * kHalf, u & 1);
-                } else if (u * kUnitTokens < len) {
-                    take_unit<NT, 2 * kUnit>(sg, page, len - u * kUnitTokens, 0);
+                } else if (u * kPage < len) {
+                    take_unit<NT, 4>(sg, page, len - u * kPage, 0);
                 }
             }
             __syncwarp();

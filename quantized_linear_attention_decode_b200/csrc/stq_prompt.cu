@@ -12,24 +12,29 @@
 namespace stq {
 namespace {
 
-// ---------------------------------------------------------------- token by token
+// ---------------------------------------------------------------- in fp32, four tokens at a time
 //
 // Columns of X do not depend on each other, so a warp owns some of them for the
 // whole prompt, in registers, and no warp waits for another but for the staged
 // tokens.  Lane (c, r) has kCols columns c and the rows that r takes of them:
-// blocks of four rows, r, r + RP, ... of the 32 blocks.  A token costs three
-// multiply-adds an element, all fp32: the two column sums X^T k and X^T q of the
-// state before the token (y follows as a X^T q + u (k . q)), then X += k u^T.
-// The decay is not multiplied in: X = c X~ with the product c of the decays, and
-// X~ is rescaled when c leaves [2^-20, 2^20], so that an element costs three packed
-// instructions a token pair in place of four.
+// blocks of four rows, r, r + RP, ... of the 32 blocks.  Tokens are taken four at a
+// time, from the state X before them: with A_j = a_0 ... a_j and D_ij = a_{i+1} ... a_j,
+//   u_j = b_j (v_j - A_j X^T k_j - sum_{i<j} D_ij (k_i . k_j) u_i)
+//   y_j = A_j X^T q_j + sum_{i<=j} D_ij (k_i . q_j) u_i
+//   X <- A_3 X + sum_i D_i3 k_i u_i^T,
+// all fp32: three multiply-adds an element and token, and one sum over a column's
+// lanes, one chain of dependent sums and one broadcast in place of four.
 // Bound by the fp32 pipe (98304 multiply-adds a token and head) when there are
-// prompts and heads enough, else by a token's latency; more lanes on a column (RP)
-// then shorten the latter.
+// prompts and heads enough, else by the latency of four tokens; more lanes on a
+// column (RP) shorten the latter.  768 units of 100 tokens take 326 us (46 TFLOP/s: two
+// warps a scheduler do not hide the sums and loads of each other), one unit 0.3 us a token.
 
 constexpr int kThreads = 128;
-constexpr int kTokens = 16;  // staged at a time
-constexpr int kCols = 4;     // columns of a lane
+constexpr int kBlock = 4;                          // tokens taken at a time
+constexpr int kTokens = kThreads / 32 * kBlock;    // staged at a time: a block a warp
+constexpr int kCols = 4;                           // columns of a lane
+constexpr int kKk = 0, kKq = 6, kSums = 16;        // of a block's coefficients: 6 and 10 inner products with their decays,
+constexpr int kDecay = 16, kGate = 20, kLast = 24; // then A_j, b_j and D_j3
 
 template <int RP>
 constexpr int kCtaCols = kThreads / RP * kCols;  // columns of a CTA
@@ -38,89 +43,109 @@ template <int RP>
 struct __align__(16) Staged {
     float k[kTokens][kD], q[kTokens][kD];
     float v[kTokens][kCtaCols<RP>];
-    // before the token X~ is multiplied by `rescale` (1: left alone); then X = c X~ with its decay, and 1 / c
-    float4 scale[kTokens];  // rescale, c, 1 / c, gate
-    float kq[kTokens];
+    float coef[kTokens / kBlock][28];
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float dot4(float4 a, float4 b) { return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w))); }
 
-// The head's rows of tokens [t0, t0 + m), as they come (zeros behind them), in the registers of all threads...
+// Halves the values that a lane holds: it keeps the lower or (with the lane's bit `o` set) the upper half,
+// summed with those of the lane across that bit.
+template <int N>
+__device__ __forceinline__ void fold(float (&x)[N], float (&to)[N / 2], int o)
+{
+    const bool upper = threadIdx.x & o;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float keep = upper ? x[i + N / 2] : x[i], give = upper ? x[i] : x[i + N / 2];
+        to[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+}
+
+// The head's rows of tokens [t0, t0 + m), as they come (zeros behind them, with decay 1 and gate 0), in the registers of all threads:
+// warp w has block w...
 template <int RP>
 struct Incoming {
-    static constexpr int kVec = kTokens * kD / 8 / kThreads, kVecV = (kTokens * kCtaCols<RP> / 8 + kThreads - 1) / kThreads;
-    float k[kVec][8], q[kVec][8], v[kVecV][8], a, b;
+    static constexpr int kVecV = kTokens * kCtaCols<RP> / 4 / kThreads;
+    float4 k[kBlock], q[kBlock], v[kVecV];
+    float a, b;  // of token lane of the block
 
     __device__ __forceinline__ void load(const PromptIO &io, int H, int h, int col0, long long t0, int m)
     {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, lane = tid & 31, mine = tid / 32 * kBlock;
+        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int t = (tid + i * kThreads) / (kD / 8), d = tid % (kD / 8) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) k[i][j] = q[i][j] = 0.0f;
-            if (t < m) {
-                load8(io.k.data, (t0 + t) * io.k.token_stride + h * io.k.head_stride + d, io.dtype, k[i]);
-                load8(io.q.data, (t0 + t) * io.q.token_stride + h * io.q.head_stride + d, io.dtype, q[i]);
-            }
+        for (int i = 0; i < kBlock; ++i) {
+            const bool there = mine + i < m;
+            k[i] = there ? load4(io.k.data, (t0 + mine + i) * io.k.token_stride + h * io.k.head_stride + 4 * lane, io.dtype) : zero;
+            q[i] = there ? load4(io.q.data, (t0 + mine + i) * io.q.token_stride + h * io.q.head_stride + 4 * lane, io.dtype) : zero;
         }
 #pragma unroll
         for (int i = 0; i < kVecV; ++i) {
-            const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 8), d = e % (kCtaCols<RP> / 8) * 8;
-            if (t < m) load8(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, io.dtype, v[i]);
+            const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 4), d = e % (kCtaCols<RP> / 4) * 4;
+            v[i] = t < m ? load4(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, io.dtype) : zero;
         }
-        a = tid < m ? io.alpha[(t0 + tid) * H + h] : 1.0f;
-        b = tid < m ? io.beta[(t0 + tid) * H + h] : 0.0f;
+        const bool there = lane < kBlock && mine + lane < m;
+        a = there ? io.alpha[(t0 + mine + lane) * H + h] : 1.0f;
+        b = there ? io.beta[(t0 + mine + lane) * H + h] : 0.0f;
     }
 
-    // ... and from there to shared memory.  c: the product of decays that X~ stands under, kept by the first warp.
-    __device__ __forceinline__ void store(Staged<RP> &s, int m, float &c) const
+    // ... and from there to shared memory, with the block's coefficients.
+    __device__ __forceinline__ void store(Staged<RP> &s) const
     {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, lane = tid & 31, block = tid / 32;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int t = (tid + i * kThreads) / (kD / 8), d = tid % (kD / 8) * 8;
-            *reinterpret_cast<float4 *>(&s.k[t][d]) = make_float4(k[i][0], k[i][1], k[i][2], k[i][3]);
-            *reinterpret_cast<float4 *>(&s.k[t][d + 4]) = make_float4(k[i][4], k[i][5], k[i][6], k[i][7]);
-            *reinterpret_cast<float4 *>(&s.q[t][d]) = make_float4(q[i][0], q[i][1], q[i][2], q[i][3]);
-            *reinterpret_cast<float4 *>(&s.q[t][d + 4]) = make_float4(q[i][4], q[i][5], q[i][6], q[i][7]);
-            float kq = 0.0f;  // 16 lanes hold a token
-#pragma unroll
-            for (int j = 0; j < 8; ++j) kq = fmaf(k[i][j], q[i][j], kq);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
-            if (tid % 16 == 0) s.kq[t] = kq;
+        for (int i = 0; i < kBlock; ++i) {
+            *reinterpret_cast<float4 *>(&s.k[block * kBlock + i][4 * lane]) = k[i];
+            *reinterpret_cast<float4 *>(&s.q[block * kBlock + i][4 * lane]) = q[i];
         }
 #pragma unroll
         for (int i = 0; i < kVecV; ++i) {
-            const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 8), d = e % (kCtaCols<RP> / 8) * 8;
-            if (t < m) {
-                *reinterpret_cast<float4 *>(&s.v[t][d]) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-                *reinterpret_cast<float4 *>(&s.v[t][d + 4]) = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-            }
+            const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 4), d = e % (kCtaCols<RP> / 4) * 4;
+            *reinterpret_cast<float4 *>(&s.v[t][d]) = v[i];
         }
-        if (tid < 32) {
-            float rescale = 1.0f, mine = 1.0f;
+        float x[kSums], x8[8], x4[4], x2[2], x1[1];
+        {
+            int to = 0;
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
-                const float next = c * __shfl_sync(0xffffffffu, a, t);
-                const bool out = !(fabsf(next) >= 0x1p-20f && fabsf(next) <= 0x1p20f);
-                if (tid == t) {
-                    rescale = out ? next : 1.0f;
-                    mine = out ? 1.0f : next;
-                }
-                c = out ? 1.0f : next;
-            }
-            if (tid < kTokens) s.scale[tid] = make_float4(rescale, mine, 1.0f / mine, b);
+            for (int i = 0; i < kBlock; ++i)
+#pragma unroll
+                for (int j = i + 1; j < kBlock; ++j) x[to++] = dot4(k[i], k[j]);
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i)
+#pragma unroll
+                for (int j = i; j < kBlock; ++j) x[to++] = dot4(k[i], q[j]);
+        }
+        fold(x, x8, 16);
+        fold(x8, x4, 8);
+        fold(x4, x2, 4);
+        fold(x2, x1, 2);  // lanes 2n and 2n + 1 have sum n
+        const float sum = x1[0] + __shfl_xor_sync(0xffffffffu, x1[0], 1);
+        // D_ij of sum n; its i and j (two bits each), in the order above
+        constexpr uint32_t kOfI = 0xe9500940u, kOfJ = 0xfb9e4fb9u;
+        const int n = lane >> 1, i = kOfI >> (2 * n) & 3, j = kOfJ >> (2 * n) & 3;
+        float decay = 1.0f, before = 1.0f, after = 1.0f;
+#pragma unroll
+        for (int m = 0; m < kBlock; ++m) {
+            const float am = __shfl_sync(0xffffffffu, a, m);
+            if (i < m && m <= j) decay *= am;
+            if (m <= lane) before *= am;
+            if (m > lane) after *= am;
+        }
+        float *c = s.coef[block];
+        if (!(lane & 1)) c[n] = decay * sum;
+        if (lane < kBlock) {
+            c[kDecay + lane] = before;
+            c[kGate + lane] = b;
+            c[kLast + lane] = after;
         }
     }
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : RP == 8 ? 3 : 4) prompt_tokens_kernel(PoolView p, PromptIO io)
+__global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kernel(PoolView p, PromptIO io)
 {
-    extern __shared__ __align__(16) uint8_t raw_smem[];
-    Staged<RP> *st = reinterpret_cast<Staged<RP> *>(raw_smem);  // two of them
+    __shared__ Staged<RP> st[2];
     constexpr int kSlices = kD / kCtaCols<RP>;
     constexpr int kBlocks = 32 / RP;  // blocks of four rows of a lane
     const int unit = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
@@ -159,93 +184,113 @@ __global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : RP == 8 ? 3 : 4) promp
             x[b][3][i] = make_float2(w[2 * i].w, w[2 * i + 1].w);
         }
     }
-    float c = 1.0f, last = 1.0f;  // X = last x; c runs ahead in the first warp
+    // X^T times the block's rows of k or q, summed over the lanes with the same lane & 3 of a column: column (lane & 3)'s
+    const auto products = [&](const float (*rows)[kD], float (&to)[kBlock]) {
+        float2 acc[kCols][kBlock];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+            for (int t = 0; t < kBlock; ++t) acc[j][t] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int t = 0; t < kBlock; ++t) {
+                const float4 w = *reinterpret_cast<const float4 *>(&rows[t][4 * (r + RP * b)]);
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    acc[j][t] = fma2(x[b][j][0], make_float2(w.x, w.y), acc[j][t]);
+                    acc[j][t] = fma2(x[b][j][1], make_float2(w.z, w.w), acc[j][t]);
+                }
+            }
+        float all[kCols * kBlock], half[2 * kBlock];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+            for (int t = 0; t < kBlock; ++t) all[j * kBlock + t] = acc[j][t].x + acc[j][t].y;
+        fold(all, half, 2);
+        fold(half, to, 1);
+    };
+
     Incoming<RP> in;
     in.load(io, p.H, h, col0, first, min(len, kTokens));
-    in.store(st[0], min(len, kTokens), c);
+    in.store(st[0]);
     __syncthreads();
     for (int t0 = 0; t0 < len; t0 += kTokens) {
         const Staged<RP> &s = st[t0 / kTokens & 1];
         const int coming = min(len - t0 - kTokens, kTokens);  // tokens after these
         if (coming > 0) in.load(io, p.H, h, col0, first + t0 + kTokens, coming);
         const int m = min(len - t0, kTokens);
-        for (int t = 0; t < m; ++t) {
-            float2 sk[kCols], sq[kCols];
+        for (int t1 = 0; t1 < m; t1 += kBlock) {
+            float sum[kBlock];
+            {
+                float both[2 * kBlock], part[kBlock];
+                products(&s.k[t1], part);
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) sk[j] = sq[j] = make_float2(0.0f, 0.0f);
-            float4 k4[kBlocks];
+                for (int t = 0; t < kBlock; ++t) both[t] = part[t];
+                products(&s.q[t1], part);
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                k4[b] = *reinterpret_cast<const float4 *>(&s.k[t][4 * (r + RP * b)]);
-                const float4 q4 = *reinterpret_cast<const float4 *>(&s.q[t][4 * (r + RP * b)]);
+                for (int t = 0; t < kBlock; ++t) both[kBlock + t] = part[t];
+                fold(both, sum, 4);  // lanes with bit 2 clear have X^T k, the others X^T q
+            }
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    sk[j] = fma2(x[b][j][0], make_float2(k4[b].x, k4[b].y), sk[j]);
-                    sk[j] = fma2(x[b][j][1], make_float2(k4[b].z, k4[b].w), sk[j]);
-                    sq[j] = fma2(x[b][j][0], make_float2(q4.x, q4.y), sq[j]);
-                    sq[j] = fma2(x[b][j][1], make_float2(q4.z, q4.w), sq[j]);
+            for (int o = 8; o < RP; o *= 2)
+#pragma unroll
+                for (int t = 0; t < kBlock; ++t) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
+            float c[28];
+#pragma unroll
+            for (int i = 0; i < 28; i += 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(&s.coef[t1 / kBlock][i]);
+                c[i] = w.x; c[i + 1] = w.y; c[i + 2] = w.z; c[i + 3] = w.w;
+            }
+            const int own = col + (r & 3);
+            // (in the lanes of X^T q, a value that nobody reads)
+            const float u0 = c[kGate] * fmaf(-c[kDecay], sum[0], s.v[t1][own]);
+            const float u1 = c[kGate + 1] * fmaf(-c[kKk], u0, fmaf(-c[kDecay + 1], sum[1], s.v[t1 + 1][own]));
+            const float u2 = c[kGate + 2] * fmaf(-c[kKk + 3], u1, fmaf(-c[kKk + 1], u0, fmaf(-c[kDecay + 2], sum[2], s.v[t1 + 2][own])));
+            const float u3 = c[kGate + 3] * fmaf(-c[kKk + 5], u2, fmaf(-c[kKk + 4], u1, fmaf(-c[kKk + 2], u0, fmaf(-c[kDecay + 3], sum[3], s.v[t1 + 3][own]))));
+            const float u[kBlock] = {u0, u1, u2, u3};
+            {
+                const int from = lane & ~(RP - 1) | r & 3;
+                float w[kBlock];
+#pragma unroll
+                for (int t = 0; t < kBlock; ++t) w[t] = __shfl_sync(0xffffffffu, u[t], from);
+                const float y[kBlock] = {fmaf(c[kKq], w[0], c[kDecay] * sum[0]),
+                                         fmaf(c[kKq + 4], w[1], fmaf(c[kKq + 1], w[0], c[kDecay + 1] * sum[1])),
+                                         fmaf(c[kKq + 7], w[2], fmaf(c[kKq + 5], w[1], fmaf(c[kKq + 2], w[0], c[kDecay + 2] * sum[2]))),
+                                         fmaf(c[kKq + 9], w[3], fmaf(c[kKq + 8], w[2], fmaf(c[kKq + 6], w[1], fmaf(c[kKq + 3], w[0], c[kDecay + 3] * sum[3]))))};
+                if ((r & ~3) == 4) {
+#pragma unroll
+                    for (int t = 0; t < kBlock; ++t)
+                        if (t1 + t < m) store_from_float(io.y, ((first + t0 + t1 + t) * p.H + h) * kD + col0 + own, io.dtype, y[t]);
                 }
             }
-            const float4 scale = s.scale[t];
-            const float kq = s.kq[t];
-            // the sums over the lanes of a column: each exchange halves the columns that a lane is left with, until
-            // lane r has column r mod 4's two
-            float vk, vq;
-            const float v = s.v[t][col + (r & 3)];
-            {
-                const bool odd = r & 1, two = r & 2;
-                float k2[2], q2[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float ke = sk[2 * j].x + sk[2 * j].y, ko = sk[2 * j + 1].x + sk[2 * j + 1].y;
-                    const float qe = sq[2 * j].x + sq[2 * j].y, qo = sq[2 * j + 1].x + sq[2 * j + 1].y;
-                    k2[j] = (odd ? ko : ke) + __shfl_xor_sync(0xffffffffu, odd ? ke : ko, 1);
-                    q2[j] = (odd ? qo : qe) + __shfl_xor_sync(0xffffffffu, odd ? qe : qo, 1);
-                }
-                vk = (two ? k2[1] : k2[0]) + __shfl_xor_sync(0xffffffffu, two ? k2[0] : k2[1], 2);
-                vq = (two ? q2[1] : q2[0]) + __shfl_xor_sync(0xffffffffu, two ? q2[0] : q2[1], 2);
-            }
-#pragma unroll
-            for (int o = 4; o < RP; o *= 2) {
-                vk += __shfl_xor_sync(0xffffffffu, vk, o);
-                vq += __shfl_xor_sync(0xffffffffu, vq, o);
-            }
-            if (scale.x != 1.0f) {  // the same for every thread of the head
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) x[b][j][i] = make_float2(x[b][j][i].x * scale.x, x[b][j][i].y * scale.x);
-                vk *= scale.x;
-                vq *= scale.x;
-            }
-            last = scale.y;
-            float own = scale.w * fmaf(-scale.y, vk, v);
-            const float y = fmaf(scale.y, vq, own * kq);
-            own *= scale.z;
-            float u[kCols];
-            {
-                const bool odd = r & 1, two = r & 2;
-                const float beside = __shfl_xor_sync(0xffffffffu, own, 1);
-                const float even = odd ? beside : own, uneven = odd ? own : beside;
-                const float even2 = __shfl_xor_sync(0xffffffffu, even, 2), uneven2 = __shfl_xor_sync(0xffffffffu, uneven, 2);
-                u[0] = two ? even2 : even;
-                u[1] = two ? uneven2 : uneven;
-                u[2] = two ? even : even2;
-                u[3] = two ? uneven : uneven2;
-            }
+            const float2 all = make_float2(c[kDecay + 3], c[kDecay + 3]), none = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
+                for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) x[b][j][i] = fma2(x[b][j][i], all, none);
+#pragma unroll
+            for (int t = 0; t < kBlock; ++t) {
+                float2 uu[kCols];
+#pragma unroll
                 for (int j = 0; j < kCols; ++j) {
-                    const float2 uu = make_float2(u[j], u[j]);
-                    x[b][j][0] = fma2(make_float2(k4[b].x, k4[b].y), uu, x[b][j][0]);
-                    x[b][j][1] = fma2(make_float2(k4[b].z, k4[b].w), uu, x[b][j][1]);
+                    const float w = c[kLast + t] * __shfl_sync(0xffffffffu, u[t], lane & ~(RP - 1) | j);
+                    uu[j] = make_float2(w, w);
                 }
-            if (r < 4) store_from_float(io.y, ((first + t0 + t) * p.H + h) * kD + col0 + col + r, io.dtype, y);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const float4 w = *reinterpret_cast<const float4 *>(&s.k[t1 + t][4 * (r + RP * b)]);
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        x[b][j][0] = fma2(make_float2(w.x, w.y), uu[j], x[b][j][0]);
+                        x[b][j][1] = fma2(make_float2(w.z, w.w), uu[j], x[b][j][1]);
+                    }
+                }
+            }
         }
-        if (coming > 0) in.store(st[(t0 / kTokens & 1) ^ 1], coming, c);
+        if (coming > 0) in.store(st[(t0 / kTokens & 1) ^ 1]);
         __syncthreads();
     }
 #pragma unroll
@@ -253,19 +298,16 @@ __global__ void __launch_bounds__(kThreads, RP == 4 ? 2 : RP == 8 ? 3 : 4) promp
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float *to = S + static_cast<size_t>(4 * (r + RP * b) + 2 * i) * kD;
-            *reinterpret_cast<float4 *>(to) = make_float4(last * x[b][0][i].x, last * x[b][1][i].x, last * x[b][2][i].x, last * x[b][3][i].x);
-            *reinterpret_cast<float4 *>(to + kD) = make_float4(last * x[b][0][i].y, last * x[b][1][i].y, last * x[b][2][i].y, last * x[b][3][i].y);
+            *reinterpret_cast<float4 *>(to) = make_float4(x[b][0][i].x, x[b][1][i].x, x[b][2][i].x, x[b][3][i].x);
+            *reinterpret_cast<float4 *>(to + kD) = make_float4(x[b][0][i].y, x[b][1][i].y, x[b][2][i].y, x[b][3][i].y);
         }
 }
 
 template <int RP>
 cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
-    const int smem = 2 * static_cast<int>(sizeof(Staged<RP>));
-    cudaError_t e = cudaFuncSetAttribute(prompt_tokens_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     const unsigned ctas = static_cast<unsigned>(io.n) * p.H * (kD / kCtaCols<RP>);
-    prompt_tokens_kernel<RP><<<ctas, kThreads, smem, stream>>>(p, io);
+    prompt_tokens_kernel<RP><<<ctas, kThreads, 0, stream>>>(p, io);
     count_launch();
     return cudaGetLastError();
 }
@@ -281,9 +323,9 @@ cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t st
         rows_mappable(io.k, p.H, total) && rows_mappable(io.v, p.H, total))
         return launch_prompt_chunks(p, io, stream);
     const long long units = static_cast<long long>(io.n) * p.H;
-    // more lanes a column shorten a token (16: 880 cycles at three warps on a scheduler) and cost a fixed part of
-    // each warp's instructions; enough warps to fill the schedulers once decide
-    if (units >= 256) return launch_tokens<4>(p, io, stream);
+    // more lanes a column shorten a block's latency and cost each warp more loads and exchanges a column: 16 against
+    // 8 lanes take 64 against 78 us on 32 units of 200 tokens, 341 against 365 us on 96 of 700, but 154 against
+    // 117 us on 128 of 200
     return units >= 128 ? launch_tokens<8>(p, io, stream) : launch_tokens<16>(p, io, stream);
 }
 

@@ -97,16 +97,6 @@ __device__ __forceinline__ void mma_f16_from(float (&d)[4], float c0, float c1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// D += A B of rows 0 to 7 alone (a0, a1: the k halves of row g).
-__device__ __forceinline__ void mma_f16_rows(float (&d)[2], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1)
-{
-    asm(
-        "{\n\t.reg .f32 u, v;\n\t"
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, u, v}, {%2, %4, %3, %4}, {%5, %6}, {%0, %1, %7, %7};\n\t}"
-        : "+f"(d[0]), "+f"(d[1])
-        : "r"(a0), "r"(a1), "r"(0u), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
 // The transpose of an 8 x 8 matrix of 16-bit values spread over a warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 {
@@ -120,13 +110,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// One element of a row of type `dtype`, and its store (rounded once, to nearest even).
-__device__ __forceinline__ float load_as_float(const void *p, int64_t i, int dtype)
-{
-    if (dtype == STQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    if (dtype == STQ_F16) return __half2float(static_cast<const __half *>(p)[i]);
-    return static_cast<const float *>(p)[i];
-}
+// The store of one element of a row of type `dtype` (rounded once, to nearest even).
 __device__ __forceinline__ void store_from_float(void *p, int64_t i, int dtype, float x)
 {
     if (dtype == STQ_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
@@ -157,6 +141,17 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, int dtype, float
             x[2 * j + 1] = f.y;
         }
     }
+}
+
+// Four of them.
+__device__ __forceinline__ float4 load4(const void *p, int64_t i, int dtype)
+{
+    if (dtype == STQ_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    if (dtype == STQ_BF16)
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 }  // namespace stq
