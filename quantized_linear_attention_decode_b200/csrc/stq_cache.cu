@@ -785,24 +785,12 @@ cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s)
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // the join's prologue may run while the last CTAs finish
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.n) * a.heads);
     // a warp of the join for every four partials that an even batch leaves a segment
     const long long partials = a.warps / std::max(1ll, static_cast<long long>(a.n) * a.c.heads * a.blocks);
     int join_warps = 2;
     while (join_warps < kMostJoinWarps && join_warps * 4 < partials) join_warps *= 2;
-    cfg.blockDim = dim3(join_warps * 32);
-    cfg.dynamicSmemBytes = join_floats(join_warps, a.warps) * sizeof(float);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel<NT>, a);
-    count_launch();
-    return e;
+    const int join_smem = static_cast<int>(join_floats(join_warps, a.warps) * sizeof(float));
+    return launch_behind(join_kernel<NT>, dim3(static_cast<unsigned>(a.n) * a.heads), join_warps * 32, join_smem, s, a);
 }
 
 stq_status check_rows(const stq_rows *r, const char *name, int32_t dtype, int32_t n)

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
     PrepSmem &s = *reinterpret_cast<PrepSmem *>(raw_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int h = blockIdx.y;
+    launch_dependents();
     if (warp == 0) {
         int e = 0, at = 0;
         const bool found = find_chunk(io, blockIdx.x, &e, &at);
@@ -227,7 +228,10 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
     }
     __syncthreads();
     const int e = s.item[0];
-    if (e < 0) return;
+    if (e < 0) {
+        wait_previous_grid();
+        return;
+    }
     const long long row0 = io.span.seq_start[e] + static_cast<long long>(s.item[1]) * kC;
     const int m = min(kC, io.span.length(e) - s.item[1] * kC);
     Prepared *out = prepared(io, H, e, s.item[1], h);
@@ -351,6 +355,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
             const float2 y = *reinterpret_cast<const float2 *>(&s.m.t[t][col]);
             *reinterpret_cast<float2 *>(out->t + block_of(i, j) + 2 * tid) = make_float2(y.x * s.beta[col], y.y * s.beta[col + 1]);
         }
+    wait_previous_grid();  // nothing here needs the states that it unpacks, but what comes behind this grid does
 }
 
 // ---------------------------------------------------------------- the walk over the chunks
@@ -458,9 +463,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         sm.item[0] = blockIdx.x / H;
     }
     __syncthreads();
+    launch_dependents();
     const int e = __shfl_sync(0xffffffffu, sm.item[0], 0);
     const int req = io.req_idx[e], slot = io.slot_idx[e];
     if (req < 0 || req >= pool.R || slot < 0 || slot >= pool.S) {
+        wait_previous_grid();
         if (tid == 0) atomicOr(pool.err, kErrIndex);
         return;
     }
@@ -472,6 +479,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const bool fresh = io.span.is_fresh(e);
     float *state = io.state + (static_cast<size_t>(e) * H + h) * kD * kD;
     if (len == 0) {
+        wait_previous_grid();
         if (fresh)
             for (int i = tid; i < kD * kD / 4; i += kChunkThreads) reinterpret_cast<float4 *>(state)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         return;
@@ -508,6 +516,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+    wait_previous_grid();  // T and P, and the states that are there already
     const Prepared *prep = prepared(io, H, e, 0, h);
     bool ok = true;
     // after a wait that gave up: loads in flight land before the memory is given back (no more than one phase each is)
@@ -886,13 +895,11 @@ cudaError_t launch(const PoolView &p, const PromptIO &io, cudaStream_t stream)
     cudaError_t e = cudaFuncSetAttribute(prepare_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    prepare_kernel<BF16><<<dim3(static_cast<unsigned>(prompt_chunks(io.n, io.span.total)), static_cast<unsigned>(p.H)), kPrepThreads, prep, stream>>>(io, p.H);
-    count_launch();
-    e = cudaGetLastError();
+    // each begins while the one before it ends
+    const dim3 prepared(static_cast<unsigned>(prompt_chunks(io.n, io.span.total)), static_cast<unsigned>(p.H));
+    e = launch_behind(prepare_kernel<BF16>, prepared, kPrepThreads, prep, stream, io, p.H);
     if (e != cudaSuccess) return e;
-    chunk_kernel<BF16><<<static_cast<unsigned>(io.n) * p.H, kChunkThreads, smem, stream>>>(q, k, v, p, io);
-    count_launch();
-    return cudaGetLastError();
+    return launch_behind(chunk_kernel<BF16>, dim3(static_cast<unsigned>(io.n) * p.H), kChunkThreads, smem, stream, q, k, v, p, io);
 }
 
 }  // namespace

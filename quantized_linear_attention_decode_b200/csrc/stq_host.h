@@ -3,6 +3,7 @@
 
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -57,6 +58,26 @@ struct DeviceGuard {
 inline int dtype_bytes(int32_t dtype) { return dtype == STQ_F32 ? 4 : dtype == STQ_BF16 || dtype == STQ_F16 ? 2 : 0; }
 
 // Every head row of `r` starts on a 16-byte boundary.
+// Launches a kernel whose CTAs may start, and get as far as their wait for the previous grid, while the last CTAs
+// of the stream's previous kernel run.  Such a kernel waits in every CTA, so that its end is the end of both.
+template <typename... Args>
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, const std::common_type_t<Args> &...args)
+{
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Args(args)...);
+    count_launch();
+    return e;
+}
+
 inline bool rows_aligned(const stq_rows *r, int32_t dtype)
 {
     const int64_t per = 16 / dtype_bytes(dtype);

@@ -17,7 +17,8 @@
 
 #include <cuda_fp16.h>
 
-#include "stq_internal.h"
+#include "stq_host.h"
+#include "stq_ptx.h"
 
 namespace stq {
 namespace {
@@ -48,6 +49,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
                                                        const int32_t *slot_idx, const float *state, PromptSpan span)
 {
     __shared__ double fit_sum[8][2][kD];  // per-warp column sums of the fit (num, den)
+    wait_previous_grid();  // (where it was launched behind a prompt's kernel)
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
     const int req = req_idx[ni], slot = slot_idx[ni];
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t
 __global__ void __launch_bounds__(256) dequantize_kernel(PoolView p, const int32_t *req_idx,
                                                          const int32_t *slot_idx, float *state, PromptSpan span)
 {
+    launch_dependents();
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
     const int req = req_idx[ni], slot = slot_idx[ni];
@@ -245,6 +248,7 @@ template <int BITS>
 __global__ void __launch_bounds__(256) quantize_raw_kernel(PoolView p, const int32_t *req_idx,
                                                            const int32_t *slot_idx, const float *state, PromptSpan span)
 {
+    wait_previous_grid();  // (where it was launched behind a prompt's kernel)
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
     const int req = req_idx[ni], slot = slot_idx[ni];
@@ -279,6 +283,7 @@ template <int BITS>
 __global__ void __launch_bounds__(256) dequantize_raw_kernel(PoolView p, const int32_t *req_idx,
                                                              const int32_t *slot_idx, float *state, PromptSpan span)
 {
+    launch_dependents();
     const int tile = blockIdx.x;
     const int ni = tile / p.H, h = tile - ni * p.H;
     const int req = req_idx[ni], slot = slot_idx[ni];
@@ -334,8 +339,14 @@ cudaError_t launch_duplicate_check(const int32_t *req_idx, const int32_t *slot_i
 cudaError_t launch_quantize(const PoolView &p, const int32_t *req_idx, const int32_t *slot_idx,
                             int n, const float *state, cudaStream_t stream, const PromptSpan &span)
 {
-    if (p.raw_bits == 32) quantize_raw_kernel<32><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
-    else if (p.raw_bits == 16) quantize_raw_kernel<16><<<n * p.H, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    const dim3 tiles(n * p.H);
+    if (span.seq_start != nullptr) {
+        if (p.raw_bits == 32) return launch_behind(quantize_raw_kernel<32>, tiles, 256, 0, stream, p, req_idx, slot_idx, state, span);
+        if (p.raw_bits == 16) return launch_behind(quantize_raw_kernel<16>, tiles, 256, 0, stream, p, req_idx, slot_idx, state, span);
+        return launch_behind(quantize_kernel, dim3(n * p.H, p.fit ? 1 : kQuantizeCtas), 256, 0, stream, p, req_idx, slot_idx, state, span);
+    }
+    if (p.raw_bits == 32) quantize_raw_kernel<32><<<tiles, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else if (p.raw_bits == 16) quantize_raw_kernel<16><<<tiles, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     else quantize_kernel<<<dim3(n * p.H, p.fit ? 1 : kQuantizeCtas), 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     count_launch();
     return cudaGetLastError();

@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
         return;
     }
+    launch_dependents();
     int len = io.span.length(e);
     if (len < 0) {
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
@@ -167,6 +168,10 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
     const int col = threadIdx.x / RP * kCols;  // of the CTA's
     const int col0 = slice * kCtaCols<RP>;
     float *S = io.state + static_cast<size_t>(unit) * kD * kD + col0 + col;
+
+    Incoming<RP> in;
+    in.load(io, p.H, h, col0, first, min(len, kTokens));
+    in.store(st[0]);
 
     // x[b][c][0..1]: rows 4 (r + RP b) + {0, 1} and {2, 3} of column c
     float2 x[kBlocks][kCols][2];
@@ -211,9 +216,6 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
         fold(half, to, 1);
     };
 
-    Incoming<RP> in;
-    in.load(io, p.H, h, col0, first, min(len, kTokens));
-    in.store(st[0]);
     __syncthreads();
     for (int t0 = 0; t0 < len; t0 += kTokens) {
         const Staged<RP> &s = st[t0 / kTokens & 1];
@@ -316,11 +318,12 @@ cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t st
 
 cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
-    // 16-bit rows go in chunks (of rows that a tensor map can describe), unless the prompts are so short that
-    // most of a chunk would be empty
+    // 16-bit rows (that a tensor map can describe) go in chunks of 64 tokens; below 40 tokens, whatever they are shared
+    // out into, the chunks are slower (one prompt of 37 tokens on 4 heads 25 against 23 us, of 16 on 8 heads 25 against
+    // 15 us, of 100 on 4 heads 29 against 39 us)
     const int total = io.span.total;
-    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= 16ll * io.n && rows_mappable(io.q, p.H, total) &&
-        rows_mappable(io.k, p.H, total) && rows_mappable(io.v, p.H, total))
+    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= 40 && rows_mappable(io.q, p.H, total) && rows_mappable(io.k, p.H, total) &&
+        rows_mappable(io.v, p.H, total))
         return launch_prompt_chunks(p, io, stream);
     const long long units = static_cast<long long>(io.n) * p.H;
     // more lanes a column shorten a block's latency and cost each warp more loads and exchanges a column: 16 against
