@@ -310,6 +310,39 @@ def test_graph_and_streams(heads):
     assert torch.equal(y, y2) and torch.equal(state, state2)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [2, 70])
+@pytest.mark.parametrize("lens", [[1], [3, 0, 20], [39]])
+def test_few_tokens_of_16_bits(kind, heads, lens):
+    """So few that no chunk is worth while; rows as parts of one projection, and behind them rows of NaN."""
+    s = _Prompts(lens, heads, kind, seed=12, fresh=[0] * len(lens))
+    m = sum(lens)
+    fused = torch.full((m + 1, 3, heads, 128), float("nan"), dtype=s.dt, device="cuda")
+    for i, t in enumerate((s.q, s.k, s.v)):
+        fused[:m, i] = t
+    s.q, s.k, s.v = fused[:m].unbind(1)
+    s.run()
+    stq.stq_pool_check(s.pool)
+    s.check()
+
+
+def test_two_calls_at_once():
+    """Two pools on two streams, in turn, each with its own workspace: as alone."""
+    calls = [_Prompts([300, 64, 7], 20, "bf16", seed=13), _Prompts([90, 250, 128, 1], 16, "fp16", seed=14)]
+    want = [tuple(t.clone() for t in s.run()) for s in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    work = [torch.empty(stq.stq_prompt_workspace(s.pool, s.n, s.total), dtype=torch.uint8, device="cuda") for s in calls]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, stream, w in zip(calls, streams, work):
+            with torch.cuda.stream(stream):
+                s.run(workspace=w)
+    torch.cuda.synchronize()
+    for s, (y, state) in zip(calls, want):
+        stq.stq_pool_check(s.pool)
+        assert torch.equal(s.y, y) and torch.equal(s.state, state)
+
+
 def test_after_a_split_step_and_with_debug_checks(monkeypatch):
     """A pending write-back is waited for; a (request, slot) named twice is reported when debug checks are on."""
     monkeypatch.setenv("STQ_DEBUG_CHECKS", "1")
