@@ -45,7 +45,7 @@ constexpr int kHalfTile = kTileBytes / 2;  // 64 of the 128 dims: rows of 128 by
 constexpr int kStages = 2;
 constexpr int kThreads = 384;  // three warpgroups; warps 10 and 11 only hand their registers over
 // registers a thread: 168 at launch, then 216 in the softmax warpgroups and 72 in the third (2 * 216 + 72 = 3 * 168)
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 
 struct PromptAttn {
     const int32_t *q_start, *k_start;
@@ -59,10 +59,13 @@ struct PromptAttn {
 struct __align__(1024) AttnSmem {
     uint8_t q[2][kTileBytes];
     uint8_t k[kStages][kTileBytes], v[kStages][kTileBytes];
-    unsigned long long q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    unsigned long long q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     unsigned long long s_full[2], p_full[2][2], o_full[2];  // p_full: of either half of the keys
+    unsigned long long item_full[2], item_empty[2], wanted, asked, drained;
+    uint4 answer;
     uint32_t tmem;
-    int item[8];  // sequence's first query row, its queries, first key row, keys, this CTA's first token, first head, key head
+    // sequence's first query row (-1: no more items), its queries, first key row, keys, the item's first token, block of heads
+    int item[2][8];
 };
 
 // Queries and keys of sequence i; false where a range is none.
@@ -74,7 +77,7 @@ __device__ __forceinline__ bool sequence(const PromptAttn &a, int i, int *lq, in
     return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
 }
 
-// The CTA's sequence and tokens: tiles of all sequences in order, within a sequence from its end, where
+// Sequence and tokens of a tile: tiles of all sequences in order, within a sequence from its end, where
 // a tile sees most keys.  One warp; false when there is no such tile.
 __device__ __forceinline__ bool find_item(const PromptAttn &a, int tile, int *seq, int *token)
 {
@@ -131,164 +134,256 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw_smem[];
     AttnSmem &sm = *reinterpret_cast<AttnSmem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && a.err != nullptr)
-        for (int i = threadIdx.x; i < a.n; i += kThreads) {
-            int lq, lk;
-            if (!sequence(a, i, &lq, &lk)) *a.err = STQ_ERR_INDEX;
-        }
-    if (warp == 0) {
-        int seq = 0, token = 0;
-        const bool found = find_item(a, blockIdx.x, &seq, &token);
-        if (lane == 0) {
-            sm.item[0] = found ? a.q_start[seq] : -1;
-            if (found) {
-                sm.item[1] = a.q_start[seq + 1] - a.q_start[seq];
-                sm.item[2] = a.k_start[seq];
-                sm.item[3] = a.k_start[seq + 1] - a.k_start[seq];
-                sm.item[4] = token;
-            }
-        }
-    } else if (warp == 8 && lane == 0) {
-        barrier_init(smem_addr(&sm.q_full), 1);
+    if (warp == 8 && lane == 0) {
+        const auto init = [](unsigned long long &b, uint32_t count) { barrier_init(smem_addr(&b), count); };
+        init(sm.q_full, 1);
+        init(sm.q_empty, 1);
         for (int s = 0; s < kStages; ++s) {
-            barrier_init(smem_addr(&sm.k_full[s]), 1);
-            barrier_init(smem_addr(&sm.k_empty[s]), 1);
-            barrier_init(smem_addr(&sm.v_full[s]), 1);
-            barrier_init(smem_addr(&sm.v_empty[s]), 1);
+            init(sm.k_full[s], 1);
+            init(sm.k_empty[s], 1);
+            init(sm.v_full[s], 1);
+            init(sm.v_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            barrier_init(smem_addr(&sm.s_full[i]), 1);
-            barrier_init(smem_addr(&sm.p_full[i][0]), kRows);
-            barrier_init(smem_addr(&sm.p_full[i][1]), kRows);
-            barrier_init(smem_addr(&sm.o_full[i]), 1);
+            init(sm.s_full[i], 1);
+            init(sm.p_full[i][0], kRows);
+            init(sm.p_full[i][1], kRows);
+            init(sm.o_full[i], 1);
+            init(sm.item_full[i], 1);
+            init(sm.item_empty[i], 2 + 8);
         }
+        init(sm.wanted, 1);
+        init(sm.asked, 1);
+        init(sm.drained, 1);
         fence_barrier_init();
     }
-    __syncthreads();
-    const int entry = sm.item[lane & 7];
-    const auto uniform = [&](int i) { return __shfl_sync(0xffffffffu, entry, i); };
-    const int q_row0 = uniform(0), lq = uniform(1), k_row0 = uniform(2), lk = uniform(3), token0 = uniform(4);
-    if (q_row0 < 0) return;
-    // blockIdx.y: key head and block of `pack` query heads
-    const int blocks = a.group / a.pack, kv_head = blockIdx.y / blocks, head0 = blockIdx.y * a.pack;
-    const int per_tile = kRows / a.pack;  // tokens of a query tile
-    // key tiles of each query tile: up to what its last token sees
-    int tiles[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int first = token0 + i * per_tile, last = min(first + per_tile, lq) - 1;
-        const int seen = first < lq ? min(lk, last + lk - lq + 1) : 0;
-        tiles[i] = seen > 0 ? (seen + kRows - 1) / kRows : 0;
-    }
-    const int all = max(tiles[0], tiles[1]);
     if (warp == 9) tmem_alloc(smem_addr(&sm.tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+    const int per_tile = kRows / a.pack;  // tokens of a query tile
     bool ok = true;
+
+    // Item n of this CTA, a value a lane; false: no more.  The whole warp calls these.
+    int entry = 0;
+    const auto take = [&](int n) {
+        ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.item_full[n & 1]), n >> 1 & 1));
+        if (ok) entry = sm.item[n & 1][lane & 7];
+        return ok && __shfl_sync(0xffffffffu, entry, 0) >= 0;
+    };
+    const auto taken = [&](int n) {
+        __syncwarp();
+        if (lane == 0) barrier_arrive(smem_addr(&sm.item_empty[n & 1]));
+    };
+    const auto value = [&](int i) { return __shfl_sync(0xffffffffu, entry, i); };
+    // keys that query tile i takes: up to what its last token sees
+    const auto keys_of = [&](int i) {
+        const int lq = value(1), lk = value(3), first = value(4) + i * per_tile, last = min(first + per_tile, lq) - 1;
+        return first < lq ? max(0, min(lk, last + lk - lq + 1)) : 0;
+    };
+    const auto tiles_of = [](int keys) { return (keys + kRows - 1) / kRows; };
+    // whether the key tile at j of `keys` ends in its first half
+    const auto is_short = [](int keys, int j) { return keys - j * kRows <= kRows / 2; };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8 && lane == 0 && all > 0) {
-            const uint32_t qf = smem_addr(&sm.q_full);
-            barrier_expect(qf, (tiles[0] > 0 ? kTileBytes : 0) + (tiles[1] > 0 ? kTileBytes : 0));
-            for (int i = 0; i < 2; ++i)
-                for (int half = 0; half < 2 && tiles[i] > 0; ++half)
-                    tma_load3(smem_addr(sm.q[i]) + half * kHalfTile, &q_map, qf, 64 * half, head0, q_row0 + token0 + i * per_tile);
-            int issued = 0;
-            for (int j = 0; j < all && ok; ++j, ++issued) {
-                const int s = j % kStages;
-                const uint32_t parity = (j / kStages & 1) ^ 1;
-                const uint32_t kf = smem_addr(&sm.k_full[s]), vf = smem_addr(&sm.v_full[s]);
-                ok = j < kStages || barrier_wait(smem_addr(&sm.k_empty[s]), parity);
+        if (warp == 10) {
+            // ------------------------------------------------ the items: this block's, then others that have not begun
+            const uint32_t blocks = a.heads / a.pack;
+            uint32_t x = blockIdx.x;
+            for (int n = 0, asked = 0; ok;) {
+                if (x == 0 && a.err != nullptr)
+                    for (int i = lane; i < a.n; i += 32) {
+                        int lq, lk;
+                        if (!sequence(a, i, &lq, &lk)) *a.err = STQ_ERR_INDEX;
+                    }
+                int seq = 0, token = 0;
+                if (find_item(a, static_cast<int>(x / blocks), &seq, &token)) {
+                    if (lane == 0) {
+                        int *item = sm.item[n & 1];
+                        item[0] = a.q_start[seq];
+                        item[1] = a.q_start[seq + 1] - a.q_start[seq];
+                        item[2] = a.k_start[seq];
+                        item[3] = a.k_start[seq + 1] - a.k_start[seq];
+                        item[4] = token;
+                        item[5] = static_cast<int>(x % blocks);
+                        barrier_arrive(smem_addr(&sm.item_full[n & 1]));
+                    }
+                    __syncwarp();
+                    ++n;
+                    // not before this one's loads are under way, so that no CTA keeps an item waiting that another could run
+                    ok = barrier_wait(smem_addr(&sm.wanted), (n - 1) & 1) &&
+                         (n < 2 || barrier_wait(smem_addr(&sm.item_empty[n & 1]), (n >> 1 & 1) ^ 1));
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (lane == 0) {
+                    barrier_expect(smem_addr(&sm.asked), 16);
+                    next_block(smem_addr(&sm.answer), smem_addr(&sm.asked));
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.asked), asked & 1));
                 if (!ok) break;
-                barrier_expect(kf, kTileBytes);
-                for (int half = 0; half < 2; ++half)
-                    tma_load3(smem_addr(sm.k[s]) + half * kHalfTile, &k_map, kf, 64 * half, kv_head, k_row0 + j * kRows);
-                ok = j < kStages || barrier_wait(smem_addr(&sm.v_empty[s]), parity);
-                barrier_expect(vf, kTileBytes);
-                for (int half = 0; half < 2; ++half)
-                    tma_load3(smem_addr(sm.v[s]) + half * kHalfTile, &v_map, vf, 64 * half, kv_head, k_row0 + j * kRows);
+                ++asked;
+                const bool more = next_block_is(smem_addr(&sm.answer), &x);
+                fence_async_smem();  // the next answer is written over this one
+                __syncwarp();
+                if (!more) {
+                    if (lane == 0) {
+                        sm.item[n & 1][0] = -1;
+                        barrier_arrive(smem_addr(&sm.item_full[n & 1]));
+                    }
+                    break;
+                }
             }
-            if (!ok) {  // the loads in flight land before the memory is given back
-                barrier_wait(qf, 0);
-                for (int j = max(0, issued - kStages); j < issued; ++j) {
+        }
+        if (warp == 8) {
+            // ------------------------------------------------ loads
+            int queries = 0, tile = 0;  // loads of queries and key tiles so far
+            for (int n = 0; take(n); ++n) {
+                const int tiles[2] = {tiles_of(keys_of(0)), tiles_of(keys_of(1))}, all = max(tiles[0], tiles[1]);
+                const int q_row = value(0) + value(4), k_row = value(2), block = value(5), kv_head = block / (a.group / a.pack);
+                if (lane == 0 && all > 0) {
+                    const uint32_t qf = smem_addr(&sm.q_full);
+                    ok = queries == 0 || barrier_wait(smem_addr(&sm.q_empty), (queries & 1) ^ 1);
+                    if (ok) {
+                        barrier_expect(qf, (tiles[0] > 0 ? kTileBytes : 0) + (tiles[1] > 0 ? kTileBytes : 0));
+                        for (int i = 0; i < 2; ++i)
+                            for (int half = 0; half < 2 && tiles[i] > 0; ++half)
+                                tma_load3(smem_addr(sm.q[i]) + half * kHalfTile, &q_map, qf, 64 * half, block * a.pack, q_row + i * per_tile);
+                        ++queries;
+                    }
+                    for (int j = 0; j < all && ok; ++j) {
+                        const int s = tile % kStages;
+                        const uint32_t parity = (tile / kStages & 1) ^ 1;
+                        const uint32_t kf = smem_addr(&sm.k_full[s]), vf = smem_addr(&sm.v_full[s]);
+                        ok = tile < kStages || barrier_wait(smem_addr(&sm.k_empty[s]), parity);
+                        if (!ok) break;
+                        barrier_expect(kf, kTileBytes);
+                        for (int half = 0; half < 2; ++half)
+                            tma_load3(smem_addr(sm.k[s]) + half * kHalfTile, &k_map, kf, 64 * half, kv_head, k_row + j * kRows);
+                        ok = tile < kStages || barrier_wait(smem_addr(&sm.v_empty[s]), parity);
+                        barrier_expect(vf, kTileBytes);
+                        for (int half = 0; half < 2; ++half)
+                            tma_load3(smem_addr(sm.v[s]) + half * kHalfTile, &v_map, vf, 64 * half, kv_head, k_row + j * kRows);
+                        ++tile;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) barrier_arrive(smem_addr(&sm.wanted));
+                taken(n);
+            }
+            if (!ok && lane == 0) {  // the loads in flight land before the memory is given back
+                if (queries > 0) barrier_wait(smem_addr(&sm.q_full), (queries - 1) & 1);
+                for (int j = max(0, tile - kStages); j < tile; ++j) {
                     barrier_wait(smem_addr(&sm.k_full[j % kStages]), j / kStages & 1);
                     barrier_wait(smem_addr(&sm.v_full[j % kStages]), j / kStages & 1);
                 }
             }
+            __syncwarp();
         }
         if (warp == 9) {
+            // ------------------------------------------------ products
             constexpr uint32_t type = BF16 ? 1 : 0;
-            const uint32_t qk = tc_idesc(type, kRows, kRows, false, false) | (a.negative ? 1u << 13 : 0u);
+            const uint32_t negate = a.negative ? 1u << 13 : 0u;
+            const uint32_t qk = tc_idesc(type, kRows, kRows, false, false) | negate, qk_short = tc_idesc(type, kRows, kRows / 2, false, false) | negate;
             constexpr uint32_t pv = tc_idesc(type, kRows, kD, true);
+            int queries = 0, tile = 0, done[2] = {0, 0};  // key tiles so far: of K and V, and of each query tile
+            int keys[2] = {0, 0};
             const auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
                 if (elect_one()) {
-                    const uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[j % kStages]);
+                    uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[(tile + j) % kStages]);
+                    const uint32_t desc = is_short(keys[i], j) ? qk_short : qk;
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
                         const uint32_t off = (s >> 2) * kHalfTile + (s & 3) * 32;
-                        tc_mma_ss(tmem + 128 * i, tc_desc(qa + off, 16, 1024), tc_desc(ka + off, 16, 1024), qk, s > 0);
+                        tc_mma_ss(tmem + 128 * i, tc_desc(qa + off, 16, 1024), tc_desc(ka + off, 16, 1024), desc, s > 0);
                     }
                     tc_commit(smem_addr(&sm.s_full[i]));
                 }
                 __syncwarp();
             };
-            if (all > 0) ok = barrier_wait(smem_addr(&sm.q_full), 0) && barrier_wait(smem_addr(&sm.k_full[0]), 0);
-            if (ok && all > 0) {
-                tc_fence_after();
-                for (int i = 0; i < 2; ++i)
-                    if (tiles[i] > 0) scores(i, 0);
-                if (elect_one()) tc_commit(smem_addr(&sm.k_empty[0]));
-            }
-            for (int j = 0; j < all && ok; ++j) {
-                const int s = j % kStages;
-                ok = barrier_wait(smem_addr(&sm.v_full[s]), j / kStages & 1) &&
-                     (j + 1 == all || barrier_wait(smem_addr(&sm.k_full[(j + 1) % kStages]), (j + 1) / kStages & 1));
-                if (!ok) break;
-                const int valid = lk - j * kRows;
-                if (valid < kRows) {
-                    // rows behind the sequence's last key are another sequence's or nobody's: their weights are zero,
-                    // but zero times an infinity is not
-                    for (int e = lane; e < (kRows - valid) * 8; e += 32)
-                        for (int half = 0; half < 2; ++half)
-                            *reinterpret_cast<uint4 *>(sm.v[s] + half * kHalfTile + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
-                    __syncwarp();
-                }
+            // S_i may be written over: the product that reads P in its place is done
+            const auto free_scores = [&](int i) { return done[i] == 0 || barrier_wait(smem_addr(&sm.o_full[i]), (done[i] - 1) & 1); };
+            for (int n = 0; take(n); ++n) {
+                taken(n);
+                keys[0] = keys_of(0);
+                keys[1] = keys_of(1);
+                const int tiles[2] = {tiles_of(keys[0]), tiles_of(keys[1])}, all = max(tiles[0], tiles[1]), lk = value(3);
+                if (all == 0) continue;
+                ok = barrier_wait(smem_addr(&sm.q_full), queries++ & 1) && barrier_wait(smem_addr(&sm.k_full[tile % kStages]), tile / kStages & 1);
                 for (int i = 0; i < 2 && ok; ++i) {
-                    if (j >= tiles[i]) continue;
-                    for (int half = 0; half < 2 && ok; ++half) {
-                        ok = barrier_wait(smem_addr(&sm.p_full[i][half]), j & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint32_t va = smem_addr(sm.v[s]);
-#pragma unroll
-                            for (int t = 4 * half; t < 4 * half + 4; ++t)
-                                tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
-                            if (half == 1) tc_commit(smem_addr(&sm.o_full[i]));
-                        }
+                    if (tiles[i] == 0) continue;
+                    ok = free_scores(i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(i, 0);
+                }
+                if (!ok) break;
+                if (elect_one()) tc_commit(smem_addr(&sm.k_empty[tile % kStages]));
+                __syncwarp();
+                for (int j = 0; j < all && ok; ++j) {
+                    const int s = (tile + j) % kStages, next = tile + j + 1;
+                    ok = barrier_wait(smem_addr(&sm.v_full[s]), (tile + j) / kStages & 1) &&
+                         (j + 1 == all || barrier_wait(smem_addr(&sm.k_full[next % kStages]), next / kStages & 1));
+                    if (!ok) break;
+                    if (j + 1 == all) {  // no more scores of these queries
+                        if (elect_one()) tc_commit(smem_addr(&sm.q_empty));
                         __syncwarp();
                     }
-                    if (!ok) break;
-                    if (j + 1 < tiles[i]) {  // the next scores go where P is: after the product that reads it
-                        ok = barrier_wait(smem_addr(&sm.o_full[i]), j & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(i, j + 1);
+                    const int valid = lk - j * kRows;
+                    if (valid < kRows) {
+                        // rows behind the sequence's last key are another sequence's or nobody's: their weights are zero,
+                        // but zero times an infinity is not
+                        for (int e = lane; e < (kRows - valid) * 8; e += 32)
+                            for (int half = 0; half < 2; ++half)
+                                *reinterpret_cast<uint4 *>(sm.v[s] + half * kHalfTile + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                        __syncwarp();
                     }
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        if (j >= tiles[i]) continue;
+                        const bool first_half = is_short(keys[i], j);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = barrier_wait(smem_addr(&sm.p_full[i][half]), done[i] & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                uint32_t va = smem_addr(sm.v[s]);
+                                if (half == 0 || !first_half) {
+#pragma unroll
+                                    for (int t = 4 * half; t < 4 * half + 4; ++t)
+                                        tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, tc_desc(va + t * 2048, kHalfTile, 1024), pv, j > 0 || t > 0);
+                                }
+                                if (half == 1) tc_commit(smem_addr(&sm.o_full[i]));
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        ++done[i];
+                        if (j + 1 < tiles[i]) {  // the next scores go where P is
+                            ok = free_scores(i);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(i, j + 1);
+                        }
+                    }
+                    if (ok && elect_one()) {
+                        tc_commit(smem_addr(&sm.v_empty[s]));
+                        if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[next % kStages]));
+                    }
+                    __syncwarp();
                 }
-                if (ok && elect_one()) {
-                    tc_commit(smem_addr(&sm.v_empty[s]));
-                    if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[(j + 1) % kStages]));
-                }
-                __syncwarp();
+                if (!ok) break;
+                tile += all;
             }
-            if (!ok && elect_one()) {  // products in flight end before the memory is given back
-                tc_commit(smem_addr(&sm.q_full));
-                barrier_wait(smem_addr(&sm.q_full), 1);
+            if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
+                tc_commit(smem_addr(&sm.drained));
+                barrier_wait(smem_addr(&sm.drained), 0);
             }
             __syncwarp();
         }
@@ -297,86 +392,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * i + lanes, to = tmem + 256 + 128 * i + lanes;
-        const int token = token0 + i * per_tile + row / a.pack;
-        const int sees = min(lk, token + lk - lq + 1);  // keys that this row sees (none: <= 0)
-        const int least = min(lk, token0 + i * per_tile + lk - lq + 1);  // that the tile's first row sees
         const float c = a.scale_log2;
-        float top = -INFINITY, sum = 0.0f;  // in units of log 2: P = exp2(c s - top)
-        for (int j = 0; j < tiles[i] && ok; ++j) {
-            ok = barrier_wait(smem_addr(&sm.s_full[i]), j & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t x[4][32];
+        int done = 0;  // key tiles so far
+        for (int n = 0; take(n); ++n) {
+            const int keys = keys_of(i), tiles = tiles_of(keys);
+            const int sees = min(value(3), value(4) + i * per_tile + row / a.pack + value(3) - value(1) + 1);  // keys that this row sees (none: <= 0)
+            const int least = min(value(3), value(4) + i * per_tile + value(3) - value(1) + 1);  // that the tile's first row sees
+            float top = -INFINITY, sum = 0.0f;  // in units of log 2: P = exp2(c s - top)
+            for (int j = 0; j < tiles && ok; ++j, ++done) {
+                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.s_full[i]), done & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const bool first_half = is_short(keys, j);
+                uint32_t x[4][32];
+                tmem_load32(ts, x[0]);
+                tmem_load32(ts + 32, x[1]);
+                if (!first_half) {
+                    tmem_load32(ts + 64, x[2]);
+                    tmem_load32(ts + 96, x[3]);
+                }
+                tmem_wait_load();
+                if ((j + 1) * kRows > least) {  // some row of the tile does not see all of these keys
+                    const int limit = sees - j * kRows;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_load32(ts + 32 * b, x[b]);
-            tmem_wait_load();
-            if ((j + 1) * kRows > least) {  // some row of the tile does not see all of these keys
-                const int limit = sees - j * kRows;
+                    for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * b + e >= limit) x[b][e] = 0xff800000u;
+                }
+                float ms[4];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * b + e >= limit) x[b][e] = 0xff800000u;
-            }
-            float ms[4];
+                for (int b = 0; b < 4; ++b) {
+                    ms[b] = fmaxf(f_of(x[b][0]), f_of(x[b][1]));
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                ms[b] = fmaxf(f_of(x[b][0]), f_of(x[b][1]));
+                    for (int e = 2; e < 32; e += 2) ms[b] = max3(ms[b], f_of(x[b][e]), f_of(x[b][e + 1]));
+                }
+                const float m = max3(fmaxf(ms[0], ms[1]), ms[2], ms[3]) * c;
+                const bool moves = m > top + 8.0f;
+                if (__any_sync(0xffffffffu, moves)) {
+                    const float now = moves ? m : top;
+                    const float f = top == -INFINITY ? 0.0f : exp2_approx(top - now);
+                    top = now;
+                    sum *= f;
+                    if (j > 0) {
+#pragma unroll 1  // (unrolled, it spills registers)
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t o[32];
+                            tmem_load32(to + 32 * b, o);
+                            tmem_wait_load();
 #pragma unroll
-                for (int e = 2; e < 32; e += 2) ms[b] = max3(ms[b], f_of(x[b][e]), f_of(x[b][e + 1]));
-            }
-            const float m = max3(fmaxf(ms[0], ms[1]), ms[2], ms[3]) * c;
-            const bool moves = m > top + 8.0f;
-            if (__any_sync(0xffffffffu, moves)) {
-                const float now = moves ? m : top;
-                const float f = top == -INFINITY ? 0.0f : exp2_approx(top - now);
-                top = now;
-                sum *= f;
-                if (j > 0) {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t o[32];
-                        tmem_load32(to + 32 * b, o);
-                        tmem_wait_load();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f_of(o[e]) * f);
-                        tmem_store32(to + 32 * b, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f_of(o[e]) * f);
+                            tmem_store32(to + 32 * b, o);
+                        }
                     }
                 }
-            }
-            const float off = top == -INFINITY ? 0.0f : -top;
-            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                const float off = top == -INFINITY ? 0.0f : -top;
+                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t w[32];
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 0 || !first_half) {
+                        uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const uint32_t *s = &x[2 * half + (e >> 4)][2 * (e & 15)];
-                    float2 z = __ffma2_rn(make_float2(f_of(s[0]), f_of(s[1])), make_float2(c, c), make_float2(off, off));
-                    z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-                    part[e & 1] = __fadd2_rn(part[e & 1], z);
-                    w[e] = pack2<BF16>(z.x, z.y);
+                        for (int e = 0; e < 32; ++e) {
+                            const uint32_t *s = &x[2 * half + (e >> 4)][2 * (e & 15)];
+                            float2 z = __ffma2_rn(make_float2(f_of(s[0]), f_of(s[1])), make_float2(c, c), make_float2(off, off));
+                            z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                            part[e & 1] = __fadd2_rn(part[e & 1], z);
+                            w[e] = pack2<BF16>(z.x, z.y);
+                        }
+                        tmem_store32(ts + 32 * half, w);
+                        tmem_wait_store();
+                        tc_fence_before();
+                    }
+                    barrier_arrive(smem_addr(&sm.p_full[i][half]));
                 }
-                tmem_store32(ts + 32 * half, w);
-                tmem_wait_store();
-                tc_fence_before();
-                barrier_arrive(smem_addr(&sm.p_full[i][half]));
+                sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
             }
-            sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
-        }
-        if (ok && tiles[i] > 0) ok = barrier_wait(smem_addr(&sm.o_full[i]), (tiles[i] - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
+            if (ok && tiles > 0) ok = barrier_wait(smem_addr(&sm.o_full[i]), (done - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             tc_fence_after();
             const float f = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that sees no key is zero
-            uint16_t *y = static_cast<uint16_t *>(a.y) + (static_cast<int64_t>(q_row0 + token) * a.heads + head0 + row % a.pack) * kD;
+            const int token = value(4) + i * per_tile + row / a.pack, lq = value(1);
+            uint16_t *y = static_cast<uint16_t *>(a.y) + (static_cast<int64_t>(value(0) + token) * a.heads + value(5) * a.pack + row % a.pack) * kD;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 uint32_t o[32];
-                if (tiles[i] > 0) {
+                if (tiles > 0) {
                     tmem_load32(to + 32 * b, o);
                     tmem_wait_load();
                 }
@@ -391,6 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            tc_fence_before();  // the next products go over what was read here
+            taken(n);
         }
     }
     if (!ok && a.err != nullptr) *a.err = STQ_ERR_TIMEOUT;
@@ -439,7 +543,7 @@ extern "C" stq_status stq_attn_prompt(const int32_t *q_start, const int32_t *k_s
     int pack = 1;  // the largest power of two that divides the group, up to a tile's rows
     while (pack < stq::kRows && group % (2 * pack) == 0) pack *= 2;
     const long long tiles = (static_cast<long long>(total_q) * pack + 2 * stq::kRows - 1) / (2 * stq::kRows) + n;
-    if (tiles > 0x7FFFFFFFll || num_heads / pack > 65535) return fail_status(STQ_ERR_ARG, "too many query tiles or heads");
+    if (tiles * (num_heads / pack) > 0x7FFFFFFFll) return fail_status(STQ_ERR_ARG, "too many query tiles or heads");
     if (n == 0 || total_q == 0) return STQ_OK;
     if (stq::fault("launch")) return fail_status(STQ_ERR_CUDA, "injected launch failure (STQ_FAULT=launch)");
     cudaPointerAttributes where;
@@ -474,7 +578,7 @@ extern "C" stq_status stq_attn_prompt(const int32_t *q_start, const int32_t *k_s
     const int smem = static_cast<int>(sizeof(stq::AttnSmem)) + 1024;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return stq::cuda_fail(e, "prompt attention attribute");
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(num_heads / pack));
+    const unsigned grid = static_cast<unsigned>(tiles * (num_heads / pack));
     kernel<<<grid, stq::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(qm, km, vm, a);
     stq::count_launch();
     e = cudaGetLastError();

@@ -110,6 +110,30 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Asks for a block of this grid that has not begun, to be run by this CTA in its place: 16 bytes come to `answer`
+// (on barrier `bar`).  After a refusal no CTA may ask again.
+__device__ __forceinline__ void next_block(uint32_t answer, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer), "r"(bar) : "memory");
+}
+
+// The answer: false, or the block's index.
+__device__ __forceinline__ bool next_block_is(uint32_t answer, uint32_t *x)
+{
+    uint32_t yes, bx;
+    asm volatile(
+        "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t.reg .b32 u, v, w;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, u, v, w}, a;\n\t}"
+        : "=r"(yes), "=r"(bx)
+        : "r"(answer)
+        : "memory");
+    *x = bx;
+    return yes != 0;
+}
+
 // The store of one element of a row of type `dtype` (rounded once, to nearest even).
 __device__ __forceinline__ void store_from_float(void *p, int64_t i, int dtype, float x)
 {
