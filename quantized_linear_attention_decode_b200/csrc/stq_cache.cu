@@ -52,12 +52,15 @@ struct Rows {
 // 8 dims a lane, so that a group of 32 values is four lanes.  Bound by memory
 // (the rows in, 144 bytes out); not tuned further.
 
-// The 16 bits of four codes, and back.
-__device__ __forceinline__ uint32_t pack4(const int *z)
+// Four codes as 16 bits of the word, from numbers kCode + z: their bits are those of kCode plus z, and so are sums of them.
+constexpr float kCode = 0x1.8p23f + 8.0f;
+__device__ __forceinline__ uint32_t pack4(const float *t)
 {
-    return static_cast<uint32_t>(z[0] + 8 | (z[1] + 8) << 4 | (z[2] + 8) << 8 | (z[3] + 8) << 12);
+    constexpr uint32_t kBits = 0x4b400000u;  // of kCode - 8
+    return __float_as_uint(t[0]) + (__float_as_uint(t[1]) << 4) + (__float_as_uint(t[2]) << 8) + (__float_as_uint(t[3]) << 12) - kBits * 0x1111u;
 }
 
+// ... and back.
 __device__ __forceinline__ void unpack4(uint32_t w, float *z)
 {
 #pragma unroll
@@ -66,9 +69,9 @@ __device__ __forceinline__ void unpack4(uint32_t w, float *z)
 
 __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long long *slot, int n, int dtype, Rows k, Rows v)
 {
-    const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(n) * c.heads) return;
-    const int i = static_cast<int>(item / c.heads), h = static_cast<int>(item - static_cast<long long>(i) * c.heads);
+    const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item >= static_cast<uint32_t>(n) * c.heads) return;
+    const int i = static_cast<int>(item / c.heads), h = static_cast<int>(item - i * static_cast<uint32_t>(c.heads));
     const int lane = threadIdx.x & 31, l = lane & 15;
     const bool key = lane < 16;
     const long long at = slot[i];
@@ -80,30 +83,34 @@ __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long lon
     const Rows &r = key ? k : v;
     float x[8];
     load8(r.data, i * r.token_stride + h * r.head_stride + 8 * l, dtype, x);
-    float a = 0.0f;
-    bool bad = false;
+    // the largest size, by its bits: an infinity or a NaN is above all
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        a = fmaxf(a, fabsf(x[j]));
-        bad |= !isfinite(x[j]);
-    }
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    const uint32_t mine = __ballot_sync(0xffffffffu, bad);
-    __half s = __float2half_rn(__fdiv_rn(a, 7.0f));
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    __half s = __float2half_rn(__fdiv_rn(__uint_as_float(top), 7.0f));
     float sf = __half2float(s);
-    if ((mine >> (lane & ~3) & 15u) != 0 || !isfinite(sf)) {
+    if (top >= 0x7f800000u || !isfinite(sf)) {
         s = __float2half_rn(0.0f);
         sf = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
         if ((lane & 3) == 0) atomicOr(c.err, kErrNonFinite);
     }
-    int z[8];
-    const float inv = __frcp_rn(sf);
+    // kCode + rint(x / s): x times the reciprocal is within 2^-15 of the quotient, which decides unless it lies that near a
+    // tie; the division is made only then.  A normal s is within 2^-11 of max / 7, so that no quotient is above 7.01; a
+    // subnormal one's are clipped.
+    float z[8], off = 0.0f;
+    const float inv = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float y = sf > 0.0f ? rounded_quotient(x[j], sf, inv) : 0.0f;
-        z[j] = static_cast<int>(fminf(fmaxf(y, -7.0f), 7.0f));
+        z[j] = fmaf(x[j], inv, kCode);
+        off = fmaxf(off, fabsf(fmaf(x[j], inv, kCode - z[j])));
     }
+    if (off > 0.4999f || (sf < 0x1p-14f && sf > 0.0f))
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = kCode + fminf(fmaxf(rintf(__fdiv_rn(x[j], sf)), -7.0f), 7.0f);
     const int o = static_cast<int>(at & (kHalf - 1)), g = l >> 2, t = l & 3;
     uint8_t *b = c.block(static_cast<int>(at / kPage), h) + (at & kHalf ? kHalfBlock : 0);
     if (key) {
@@ -121,9 +128,9 @@ __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long lon
 
 __global__ void __launch_bounds__(256) read_kernel(CacheView c, const long long *slot, int n, float *k, float *v)
 {
-    const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(n) * c.heads) return;
-    const int i = static_cast<int>(item / c.heads), h = static_cast<int>(item - static_cast<long long>(i) * c.heads);
+    const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item >= static_cast<uint32_t>(n) * c.heads) return;
+    const int i = static_cast<int>(item / c.heads), h = static_cast<int>(item - i * static_cast<uint32_t>(c.heads));
     const int lane = threadIdx.x & 31, l = lane & 15;
     const bool key = lane < 16;
     const long long at = slot[i];
