@@ -48,9 +48,10 @@ struct Rows {
 
 // ---------------------------------------------------------------- append and read
 //
-// A warp takes one token of one key head: lanes 0-15 its key, 16-31 its value,
-// 8 dims a lane, so that a group of 32 values is four lanes.  Bound by memory
-// (the rows in, 144 bytes out); not tuned further.
+// An item is one token of one key head.  To read, a warp takes one: lanes 0-15 its key,
+// 16-31 its value, 8 dims a lane.  To append, a warp takes two, 16 dims a lane, so that a
+// group of 32 values is two lanes: bound by instructions (a warp with one item took 300, and
+// 17.5 us for 6600 tokens of 8 heads; two 16 us).
 
 // Four codes as 16 bits of the word, from numbers kCode + z: their bits are those of kCode plus z, and so are sums of them.
 constexpr float kCode = 0x1.8p23f + 8.0f;
@@ -69,60 +70,64 @@ __device__ __forceinline__ void unpack4(uint32_t w, float *z)
 
 __global__ void __launch_bounds__(256) append_kernel(CacheView c, const long long *slot, int n, int dtype, Rows k, Rows v)
 {
-    const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (item >= static_cast<uint32_t>(n) * c.heads) return;
+    const int lane = threadIdx.x & 31, l = lane & 7;
+    const uint32_t item = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 2 + (lane >> 4);
+    const bool key = !(lane & 8);
     const int i = static_cast<int>(item / c.heads), h = static_cast<int>(item - i * static_cast<uint32_t>(c.heads));
-    const int lane = threadIdx.x & 31, l = lane & 15;
-    const bool key = lane < 16;
-    const long long at = slot[i];
-    if (at < 0) return;
-    if (at >= static_cast<long long>(c.pages) * kPage) {
-        if (lane == 0) atomicOr(c.err, kErrIndex);
-        return;
-    }
+    const bool there = item < static_cast<uint32_t>(n) * c.heads;
+    const long long at = there ? slot[i] : -1;
+    if (there && at >= static_cast<long long>(c.pages) * kPage && l == 0 && key) atomicOr(c.err, kErrIndex);
+    const bool held = at >= 0 && at < static_cast<long long>(c.pages) * kPage;
     const Rows &r = key ? k : v;
-    float x[8];
-    load8(r.data, i * r.token_stride + h * r.head_stride + 8 * l, dtype, x);
+    float x[16];
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (held) load8(r.data, i * r.token_stride + h * r.head_stride + 16 * l + 8 * part, dtype, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[8 * part + j] = y[j];
+    }
     // the largest size, by its bits: an infinity or a NaN is above all
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (!held) return;
     __half s = __float2half_rn(__fdiv_rn(__uint_as_float(top), 7.0f));
     float sf = __half2float(s);
     if (top >= 0x7f800000u || !isfinite(sf)) {
         s = __float2half_rn(0.0f);
         sf = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-        if ((lane & 3) == 0) atomicOr(c.err, kErrNonFinite);
+        for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+        if ((lane & 1) == 0) atomicOr(c.err, kErrNonFinite);
     }
-    // kCode + rint(x / s): x times the reciprocal is within 2^-15 of the quotient, which decides unless it lies that near a
-    // tie; the division is made only then.  A normal s is within 2^-11 of max / 7, so that no quotient is above 7.01; a
+    // kCode + rint(x / s): x times the reciprocal and the quotient are each within 7.01 * 2^-24 of x / s, which decides unless
+    // they lie within 2^-20 of a tie; the division is made only then.  A normal s is within 2^-11 of max / 7, so that no quotient is above 7.01; a
     // subnormal one's are clipped.
-    float z[8], off = 0.0f;
+    float z[16], off = 0.0f;
     const float inv = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
         z[j] = fmaf(x[j], inv, kCode);
         off = fmaxf(off, fabsf(fmaf(x[j], inv, kCode - z[j])));
     }
-    if (off > 0.4999f || (sf < 0x1p-14f && sf > 0.0f))
+    if (off > 0.499998f || (sf < 0x1p-14f && sf > 0.0f))
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = kCode + fminf(fmaxf(rintf(__fdiv_rn(x[j], sf)), -7.0f), 7.0f);
-    const int o = static_cast<int>(at & (kHalf - 1)), g = l >> 2, t = l & 3;
-    uint8_t *b = c.block(static_cast<int>(at / kPage), h) + (at & kHalf ? kHalfBlock : 0);
+        for (int j = 0; j < 16; ++j) z[j] = kCode + fminf(fmaxf(rintf(__fdiv_rn(x[j], sf)), -7.0f), 7.0f);
+    // dims 32 g + 16 u and on
+    const int o = static_cast<int>(at & (kHalf - 1)), g = l >> 1, u = l & 1;
+    uint8_t *b = c.block(static_cast<int>(at / kPage), h) + (at & kHalf ? kHalfBlock : 0) + 4 * g;
     if (key) {
-        *reinterpret_cast<uint32_t *>(b + 64 * o + 16 * t + 4 * g) = pack4(z) | pack4(z + 4) << 16;
-        if (t == 0) *reinterpret_cast<__half *>(b + kKeyScales + 8 * o + 2 * g) = s;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) *reinterpret_cast<uint32_t *>(b + 64 * o + 16 * (2 * u + w)) = pack4(z + 8 * w) | pack4(z + 8 * w + 4) << 16;
+        if (u == 0) *reinterpret_cast<__half *>(b - 2 * g + kKeyScales + 8 * o) = s;
     } else {
         const int p = o >> 1;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-            *reinterpret_cast<uint16_t *>(b + kValues + 128 * p + 16 * ((2 * t + half + 2 * p) & 7) + 4 * g + 2 * (o & 1)) =
-                static_cast<uint16_t>(pack4(z + 4 * half));
-        if (t == 0) *reinterpret_cast<__half *>(b + kValueScales + 16 * p + 4 * g + 2 * (o & 1)) = s;
+        for (int w = 0; w < 4; ++w)
+            *reinterpret_cast<uint16_t *>(b + kValues + 128 * p + 16 * ((4 * u + w + 2 * p) & 7) + 2 * (o & 1)) = static_cast<uint16_t>(pack4(z + 4 * w));
+        if (u == 0) *reinterpret_cast<__half *>(b + kValueScales + 16 * p + 2 * (o & 1)) = s;
     }
 }
 
@@ -883,7 +888,7 @@ stq_status stq_cache_append(stq_cache *c, const int64_t *slot, int32_t n, int32_
     stq::DeviceGuard g(c->device);
     stq::NvtxRange nvtx("stq_cache_append");
     if (!g.ok) return fail_status(STQ_ERR_CUDA, "cannot select device %d", c->device);
-    const unsigned ctas = static_cast<unsigned>((static_cast<long long>(n) * c->heads + 7) / 8);
+    const unsigned ctas = static_cast<unsigned>((static_cast<long long>(n) * c->heads + 15) / 16);
     stq::append_kernel<<<ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         stq::view(c), reinterpret_cast<const long long *>(slot), n, dtype, stq::rows(k), stq::rows(v));
     stq::count_launch();
