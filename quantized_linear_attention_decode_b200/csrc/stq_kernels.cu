@@ -43,7 +43,7 @@ __device__ __forceinline__ uint8_t *tile_page(const PoolView &p, int req, int sl
 // v_ij = s_i r_i z_ij (each term formed in the oracle's operation order), and
 // stored in the page.  One warp per row; without the fit a tile's rows do not meet, and
 // kQuantizeCtas CTAs share them (768 tiles: 75 us with one CTA a tile and every quotient
-// divided, 4 tiles 26 us).
+// divided, 39 so; 4 tiles 26 and 7 us).
 constexpr int kQuantizeCtas = 4;
 __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t *req_idx,
                                                        const int32_t *slot_idx, const float *state, PromptSpan span)
