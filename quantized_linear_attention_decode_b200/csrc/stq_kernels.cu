@@ -42,9 +42,7 @@ __device__ __forceinline__ uint8_t *tile_page(const PoolView &p, int req, int sl
 // non-pivot rows in fp64, c_j = sum_i w_i^2 v_ij S_ij / sum_i w_i^2 v_ij^2 with
 // v_ij = s_i r_i z_ij (each term formed in the oracle's operation order), and
 // stored in the page.  One warp per row; without the fit a tile's rows do not meet, and
-// kQuantizeCtas CTAs share them (768 tiles: 75 us with one CTA a tile and every quotient
-// divided, 39 so; 4 tiles 26 and 7 us).
-constexpr int kQuantizeCtas = 4;
+// several CTAs share them (768 tiles: 75 us with one CTA a tile and every quotient divided, 34 so).
 __global__ void __launch_bounds__(256) quantize_kernel(PoolView p, const int32_t *req_idx,
                                                        const int32_t *slot_idx, const float *state, PromptSpan span)
 {
@@ -336,6 +334,15 @@ cudaError_t launch_duplicate_check(const int32_t *req_idx, const int32_t *slot_i
     return cudaGetLastError();
 }
 
+// CTAs of a tile: enough to spread few tiles over the SMs, and no more, since each fetches the tile's columns.
+// 16, 8, 4 and 2 of them take 2.7, 3.5, 4.9 and 8.0 us on 4 tiles, 4.6, 3.9, 5.3 and 8.4 on 32, 18, 15, 15 and 16 on 256,
+// 152, 113, 93 and 84 on 2048.
+int quantize_ctas(const PoolView &p, int n)
+{
+    const int tiles = n * p.H;
+    return p.fit ? 1 : tiles <= 16 ? 16 : tiles <= 32 ? 8 : tiles <= 512 ? 4 : 2;
+}
+
 cudaError_t launch_quantize(const PoolView &p, const int32_t *req_idx, const int32_t *slot_idx,
                             int n, const float *state, cudaStream_t stream, const PromptSpan &span)
 {
@@ -343,11 +350,11 @@ cudaError_t launch_quantize(const PoolView &p, const int32_t *req_idx, const int
     if (span.seq_start != nullptr) {
         if (p.raw_bits == 32) return launch_behind(quantize_raw_kernel<32>, tiles, 256, 0, stream, p, req_idx, slot_idx, state, span);
         if (p.raw_bits == 16) return launch_behind(quantize_raw_kernel<16>, tiles, 256, 0, stream, p, req_idx, slot_idx, state, span);
-        return launch_behind(quantize_kernel, dim3(n * p.H, p.fit ? 1 : kQuantizeCtas), 256, 0, stream, p, req_idx, slot_idx, state, span);
+        return launch_behind(quantize_kernel, dim3(n * p.H, quantize_ctas(p, n)), 256, 0, stream, p, req_idx, slot_idx, state, span);
     }
     if (p.raw_bits == 32) quantize_raw_kernel<32><<<tiles, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     else if (p.raw_bits == 16) quantize_raw_kernel<16><<<tiles, 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
-    else quantize_kernel<<<dim3(n * p.H, p.fit ? 1 : kQuantizeCtas), 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
+    else quantize_kernel<<<dim3(n * p.H, quantize_ctas(p, n)), 256, 0, stream>>>(p, req_idx, slot_idx, state, span);
     count_launch();
     return cudaGetLastError();
 }
