@@ -89,28 +89,29 @@ __device__ __forceinline__ bool sequence(const PromptAttn &a, int i, int *lq, in
 
 // Sequence and tokens of a tile: tiles of all sequences in order, within a sequence from its end, where
 // a tile sees most keys.  One warp; false when there is no such tile.
-__device__ __forceinline__ bool find_item(const PromptAttn &a, int tile, int *seq, int *token)
+// `from` and `base`: where the last search began to find its tile, and the tiles before there; blocks mostly come in order.
+__device__ __forceinline__ bool find_item(const PromptAttn &a, int tile, int *from, long long *base, int *seq, int *token)
 {
     const int lane = threadIdx.x & 31, tokens = 2 * kRows / a.pack;
-    long long base = 0;
-    for (int first = 0; first < a.n; first += 32) {
+    if (tile < *base) *from = *base = 0;
+    for (; *from < a.n; *from += 32) {
         int lq = 0, lk, mine = 0;
-        if (first + lane < a.n && sequence(a, first + lane, &lq, &lk)) mine = (lq + tokens - 1) / tokens;
+        if (*from + lane < a.n && sequence(a, *from + lane, &lq, &lk)) mine = (lq + tokens - 1) / tokens;
         long long upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += x;
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, base + upto > tile);
+        const uint32_t past = __ballot_sync(0xffffffffu, *base + upto > tile);
         if (past) {
             const int who = __ffs(past) - 1;
-            const long long end = base + __shfl_sync(0xffffffffu, upto, who);
-            *seq = first + who;
+            const long long end = *base + __shfl_sync(0xffffffffu, upto, who);
+            *seq = *from + who;
             *token = static_cast<int>(end - 1 - tile) * tokens;
             return true;
         }
-        base += __shfl_sync(0xffffffffu, upto, 31);
+        *base += __shfl_sync(0xffffffffu, upto, 31);
     }
     return false;
 }
@@ -202,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------ the items: this block's, then others that have not begun
             const uint32_t blocks = a.heads / a.pack;
             uint32_t x = blockIdx.x;
+            int from = 0;
+            long long base = 0;
             for (int n = 0, asked = 0; ok;) {
                 if (x == 0 && a.err != nullptr)
                     for (int i = lane; i < a.n; i += 32) {
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!sequence(a, i, &lq, &lk)) *a.err = STQ_ERR_INDEX;
                     }
                 int seq = 0, token = 0;
-                if (find_item(a, static_cast<int>(x / blocks), &seq, &token)) {
+                if (find_item(a, static_cast<int>(x / blocks), &from, &base, &seq, &token)) {
                     if (lane == 0) {
                         int *item = sm.item[n & 1];
                         item[0] = a.q_start[seq];

@@ -82,6 +82,12 @@ def test_pieces(lens, prefix, heads, kv_heads):
     a.check(a.run())
 
 
+def test_many_short_prompts():
+    """Far more sequences than a warp looks at once, some of them empty."""
+    s = _Attn([(7 * i) % 5 for i in range(1500)], 4, 2)
+    s.check(s.run())
+
+
 def test_one_long_prompt():
     a = _Attn([2300], 2, 1, seed=3)
     a.check(a.run())

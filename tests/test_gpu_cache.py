@@ -183,6 +183,13 @@ def test_attend_sizes(spread, size):
     s.check(s.attend())
 
 
+def test_attend_many_sequences():
+    """More sequences than warps look at once, and more segments than shares."""
+    s = _Sequences([(37 * i) % 131 for i in range(900)], 4, 2, "bf16", seed=21)
+    s.append()
+    s.check(s.attend())
+
+
 def test_attend_values_of_mixed_sizes():
     """Tokens and groups whose values differ by orders: each dim to its own group's size."""
     s = _Sequences([900, 65], 8, 2, "bf16", seed=5)

@@ -326,6 +326,15 @@ def test_few_tokens_of_16_bits(kind, heads, lens):
     s.check()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_many_prompts(kind):
+    """More entries than the walk ranks by their length, from none to two chunks of tokens."""
+    s = _Prompts([(29 * i) % 97 for i in range(200)], 1, kind, seed=15, fresh=[i % 3 == 0 for i in range(200)])
+    s.run()
+    stq.stq_pool_check(s.pool)
+    s.check()
+
+
 def test_two_calls_at_once():
     """Two pools on two streams, in turn, each with its own workspace: as alone."""
     calls = [_Prompts([300, 64, 7], 20, "bf16", seed=13), _Prompts([90, 250, 128, 1], 16, "fp16", seed=14)]
