@@ -64,7 +64,7 @@ __device__ __forceinline__ void fold(float (&x)[N], float (&to)[N / 2], int o)
 
 // The head's rows of tokens [t0, t0 + m), as they come (zeros behind them, with decay 1 and gate 0), in the registers of all threads:
 // warp w has block w...
-template <int RP>
+template <int RP, int TYPE>
 struct Incoming {
     static constexpr int kVecV = kTokens * kCtaCols<RP> / 4 / kThreads;
     float4 k[kBlock], q[kBlock], v[kVecV];
@@ -77,13 +77,13 @@ struct Incoming {
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) {
             const bool there = mine + i < m;
-            k[i] = there ? load4(io.k.data, (t0 + mine + i) * io.k.token_stride + h * io.k.head_stride + 4 * lane, io.dtype) : zero;
-            q[i] = there ? load4(io.q.data, (t0 + mine + i) * io.q.token_stride + h * io.q.head_stride + 4 * lane, io.dtype) : zero;
+            k[i] = there ? load4(io.k.data, (t0 + mine + i) * io.k.token_stride + h * io.k.head_stride + 4 * lane, TYPE) : zero;
+            q[i] = there ? load4(io.q.data, (t0 + mine + i) * io.q.token_stride + h * io.q.head_stride + 4 * lane, TYPE) : zero;
         }
 #pragma unroll
         for (int i = 0; i < kVecV; ++i) {
             const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 4), d = e % (kCtaCols<RP> / 4) * 4;
-            v[i] = t < m ? load4(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, io.dtype) : zero;
+            v[i] = t < m ? load4(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, TYPE) : zero;
         }
         const bool there = lane < kBlock && mine + lane < m;
         a = there ? io.alpha[(t0 + mine + lane) * H + h] : 1.0f;
@@ -142,10 +142,11 @@ struct Incoming {
     }
 };
 
-template <int RP>
+template <int RP, int TYPE>
 __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kernel(PoolView p, PromptIO io)
 {
     __shared__ Staged<RP> st[2];
+    __shared__ float4 solved[2][kThreads / RP][kCols];  // u of a column's four tokens, of this block and of the last
     constexpr int kSlices = kD / kCtaCols<RP>;
     constexpr int kBlocks = 32 / RP;  // blocks of four rows of a lane
     const int unit = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
     const int col0 = slice * kCtaCols<RP>;
     float *S = io.state + static_cast<size_t>(unit) * kD * kD + col0 + col;
 
-    Incoming<RP> in;
+    Incoming<RP, TYPE> in;
     in.load(io, p.H, h, col0, first, min(len, kTokens));
     in.store(st[0]);
 
@@ -250,12 +251,12 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
             const float u1 = c[kGate + 1] * fmaf(-c[kKk], u0, fmaf(-c[kDecay + 1], sum[1], s.v[t1 + 1][own]));
             const float u2 = c[kGate + 2] * fmaf(-c[kKk + 3], u1, fmaf(-c[kKk + 1], u0, fmaf(-c[kDecay + 2], sum[2], s.v[t1 + 2][own])));
             const float u3 = c[kGate + 3] * fmaf(-c[kKk + 5], u2, fmaf(-c[kKk + 4], u1, fmaf(-c[kKk + 2], u0, fmaf(-c[kDecay + 3], sum[3], s.v[t1 + 3][own]))));
-            const float u[kBlock] = {u0, u1, u2, u3};
+            float4 *us = solved[t1 / kBlock & 1][threadIdx.x / RP];
+            if (r < kCols) us[r] = make_float4(u0, u1, u2, u3);
+            __syncwarp();
             {
-                const int from = lane & ~(RP - 1) | r & 3;
-                float w[kBlock];
-#pragma unroll
-                for (int t = 0; t < kBlock; ++t) w[t] = __shfl_sync(0xffffffffu, u[t], from);
+                const float4 w4 = us[r & 3];
+                const float w[kBlock] = {w4.x, w4.y, w4.z, w4.w};
                 const float y[kBlock] = {fmaf(c[kKq], w[0], c[kDecay] * sum[0]),
                                          fmaf(c[kKq + 4], w[1], fmaf(c[kKq + 1], w[0], c[kDecay + 1] * sum[1])),
                                          fmaf(c[kKq + 7], w[2], fmaf(c[kKq + 5], w[1], fmaf(c[kKq + 2], w[0], c[kDecay + 2] * sum[2]))),
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
                 if ((r & ~3) == 4) {
 #pragma unroll
                     for (int t = 0; t < kBlock; ++t)
-                        if (t1 + t < m) store_from_float(io.y, ((first + t0 + t1 + t) * p.H + h) * kD + col0 + own, io.dtype, y[t]);
+                        if (t1 + t < m) store_from_float(io.y, ((first + t0 + t1 + t) * p.H + h) * kD + col0 + own, TYPE, y[t]);
                 }
             }
             const float2 all = make_float2(c[kDecay + 3], c[kDecay + 3]), none = make_float2(0.0f, 0.0f);
@@ -273,24 +274,26 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
                 for (int j = 0; j < kCols; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) x[b][j][i] = fma2(x[b][j][i], all, none);
+            float u[kCols][kBlock];
 #pragma unroll
-            for (int t = 0; t < kBlock; ++t) {
-                float2 uu[kCols];
+            for (int j = 0; j < kCols; ++j) {
+                const float4 w = us[j];
+                u[j][0] = c[kLast] * w.x;
+                u[j][1] = c[kLast + 1] * w.y;
+                u[j][2] = c[kLast + 2] * w.z;
+                u[j][3] = c[kLast + 3] * w.w;
+            }
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    const float w = c[kLast + t] * __shfl_sync(0xffffffffu, u[t], lane & ~(RP - 1) | j);
-                    uu[j] = make_float2(w, w);
-                }
+            for (int t = 0; t < kBlock; ++t)
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     const float4 w = *reinterpret_cast<const float4 *>(&s.k[t1 + t][4 * (r + RP * b)]);
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
-                        x[b][j][0] = fma2(make_float2(w.x, w.y), uu[j], x[b][j][0]);
-                        x[b][j][1] = fma2(make_float2(w.z, w.w), uu[j], x[b][j][1]);
+                        x[b][j][0] = fma2(make_float2(w.x, w.y), make_float2(u[j][t], u[j][t]), x[b][j][0]);
+                        x[b][j][1] = fma2(make_float2(w.z, w.w), make_float2(u[j][t], u[j][t]), x[b][j][1]);
                     }
                 }
-            }
         }
         if (coming > 0) in.store(st[(t0 / kTokens & 1) ^ 1]);
         __syncthreads();
@@ -305,13 +308,20 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
         }
 }
 
-template <int RP>
+template <int RP, int TYPE>
 cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
     const unsigned ctas = static_cast<unsigned>(io.n) * p.H * (kD / kCtaCols<RP>);
-    prompt_tokens_kernel<RP><<<ctas, kThreads, 0, stream>>>(p, io);
+    prompt_tokens_kernel<RP, TYPE><<<ctas, kThreads, 0, stream>>>(p, io);
     count_launch();
     return cudaGetLastError();
+}
+
+template <int RP>
+cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t stream)
+{
+    if (io.dtype == STQ_F32) return launch_tokens<RP, STQ_F32>(p, io, stream);
+    return io.dtype == STQ_BF16 ? launch_tokens<RP, STQ_BF16>(p, io, stream) : launch_tokens<RP, STQ_F16>(p, io, stream);
 }
 
 }  // namespace
