@@ -24,10 +24,11 @@ namespace {
 //   X <- A_3 X + sum_i D_i3 k_i u_i^T,
 // all fp32: three multiply-adds an element and token, and one sum over a column's
 // lanes, one chain of dependent sums and one broadcast in place of four.
-// Bound by the fp32 pipe (98304 multiply-adds a token and head) when there are
-// prompts and heads enough, else by the latency of four tokens; more lanes on a
-// column (RP) shorten the latter.  768 units of 100 tokens take 326 us (46 TFLOP/s: two
-// warps a scheduler do not hide the sums and loads of each other), one unit 0.3 us a token.
+// Bound by the fp32 pipe (49152 multiply-adds a token and head) and by reads and exchanges
+// through shared memory when there are prompts and heads enough, else by the latency of
+// four tokens; more lanes on a column (RP) shorten the latter.  768 units of 100 tokens take
+// 292 us (26 TFLOP/s: half of the issue slots, two warps a scheduler do not hide each other's
+// sums and loads), one unit 0.2 us a token.
 
 constexpr int kThreads = 128;
 constexpr int kBlock = 4;                          // tokens taken at a time
@@ -328,17 +329,17 @@ cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t st
 
 cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
-    // 16-bit rows (that a tensor map can describe) go in chunks of 64 tokens; below 40 tokens, whatever they are shared
-    // out into, the chunks are slower (one prompt of 37 tokens on 4 heads 25 against 23 us, of 16 on 8 heads 25 against
-    // 15 us, of 100 on 4 heads 29 against 39 us)
+    // 16-bit rows (that a tensor map can describe) go in chunks of 64 tokens; fewer tokens than that, whatever prompts they
+    // are shared out into, are as fast or faster without (one prompt of 37 tokens on 4 heads 17 against 25 us, of 64 21 us
+    // both, of 80 25 against 23; 4 prompts of 16 tokens on 32 heads 25 against 34 us)
     const int total = io.span.total;
-    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= 40 && rows_mappable(io.q, p.H, total) && rows_mappable(io.k, p.H, total) &&
+    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= kPromptChunk && rows_mappable(io.q, p.H, total) && rows_mappable(io.k, p.H, total) &&
         rows_mappable(io.v, p.H, total))
         return launch_prompt_chunks(p, io, stream);
     const long long units = static_cast<long long>(io.n) * p.H;
     // more lanes a column shorten a block's latency and cost each warp more loads and exchanges a column: 16 against
-    // 8 lanes take 64 against 78 us on 32 units of 200 tokens, 341 against 365 us on 96 of 700, but 154 against
-    // 117 us on 128 of 200
+    // 8 lanes take 54 against 66 us on 32 units of 200 tokens, 314 against 324 us on 96 of 700, but 139 against
+    // 108 us on 128 of 200
     return units >= 128 ? launch_tokens<8>(p, io, stream) : launch_tokens<16>(p, io, stream);
 }
 
