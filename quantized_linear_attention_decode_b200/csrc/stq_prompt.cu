@@ -63,28 +63,51 @@ __device__ __forceinline__ void fold(float (&x)[N], float (&to)[N / 2], int o)
     }
 }
 
+// Four consecutive elements as they lie in memory, and as numbers.
+template <int TYPE>
+struct Four {
+    uint2 w;
+    __device__ __forceinline__ float4 wide() const
+    {
+        if (TYPE == STQ_BF16)
+            return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+};
+template <>
+struct Four<STQ_F32> {
+    float4 w;
+    __device__ __forceinline__ float4 wide() const { return w; }
+};
+template <int TYPE>
+__device__ __forceinline__ Four<TYPE> load4(const void *p, int64_t i)
+{
+    return *reinterpret_cast<const Four<TYPE> *>(static_cast<const uint8_t *>(p) + i * static_cast<int>(sizeof(Four<TYPE>) / 4));
+}
+
 // The head's rows of tokens [t0, t0 + m), as they come (zeros behind them, with decay 1 and gate 0), in the registers of all threads:
 // warp w has block w...
 template <int RP, int TYPE>
 struct Incoming {
     static constexpr int kVecV = kTokens * kCtaCols<RP> / 4 / kThreads;
-    float4 k[kBlock], q[kBlock], v[kVecV];
+    Four<TYPE> k[kBlock], q[kBlock], v[kVecV];
     float a, b;  // of token lane of the block
 
     __device__ __forceinline__ void load(const PromptIO &io, int H, int h, int col0, long long t0, int m)
     {
         const int tid = threadIdx.x, lane = tid & 31, mine = tid / 32 * kBlock;
-        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const Four<TYPE> zero = {};
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) {
             const bool there = mine + i < m;
-            k[i] = there ? load4(io.k.data, (t0 + mine + i) * io.k.token_stride + h * io.k.head_stride + 4 * lane, TYPE) : zero;
-            q[i] = there ? load4(io.q.data, (t0 + mine + i) * io.q.token_stride + h * io.q.head_stride + 4 * lane, TYPE) : zero;
+            k[i] = there ? load4<TYPE>(io.k.data, (t0 + mine + i) * io.k.token_stride + h * io.k.head_stride + 4 * lane) : zero;
+            q[i] = there ? load4<TYPE>(io.q.data, (t0 + mine + i) * io.q.token_stride + h * io.q.head_stride + 4 * lane) : zero;
         }
 #pragma unroll
         for (int i = 0; i < kVecV; ++i) {
             const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 4), d = e % (kCtaCols<RP> / 4) * 4;
-            v[i] = t < m ? load4(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d, TYPE) : zero;
+            v[i] = t < m ? load4<TYPE>(io.v.data, (t0 + t) * io.v.token_stride + h * io.v.head_stride + col0 + d) : zero;
         }
         const bool there = lane < kBlock && mine + lane < m;
         a = there ? io.alpha[(t0 + mine + lane) * H + h] : 1.0f;
@@ -95,15 +118,16 @@ struct Incoming {
     __device__ __forceinline__ void store(Staged<RP> &s) const
     {
         const int tid = threadIdx.x, lane = tid & 31, block = tid / 32;
+        float4 kw[kBlock], qw[kBlock];
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) {
-            *reinterpret_cast<float4 *>(&s.k[block * kBlock + i][4 * lane]) = k[i];
-            *reinterpret_cast<float4 *>(&s.q[block * kBlock + i][4 * lane]) = q[i];
+            *reinterpret_cast<float4 *>(&s.k[block * kBlock + i][4 * lane]) = kw[i] = k[i].wide();
+            *reinterpret_cast<float4 *>(&s.q[block * kBlock + i][4 * lane]) = qw[i] = q[i].wide();
         }
 #pragma unroll
         for (int i = 0; i < kVecV; ++i) {
             const int e = tid + i * kThreads, t = e / (kCtaCols<RP> / 4), d = e % (kCtaCols<RP> / 4) * 4;
-            *reinterpret_cast<float4 *>(&s.v[t][d]) = v[i];
+            *reinterpret_cast<float4 *>(&s.v[t][d]) = v[i].wide();
         }
         float x[kSums], x8[8], x4[4], x2[2], x1[1];
         {
@@ -111,11 +135,11 @@ struct Incoming {
 #pragma unroll
             for (int i = 0; i < kBlock; ++i)
 #pragma unroll
-                for (int j = i + 1; j < kBlock; ++j) x[to++] = dot4(k[i], k[j]);
+                for (int j = i + 1; j < kBlock; ++j) x[to++] = dot4(kw[i], kw[j]);
 #pragma unroll
             for (int i = 0; i < kBlock; ++i)
 #pragma unroll
-                for (int j = i; j < kBlock; ++j) x[to++] = dot4(k[i], q[j]);
+                for (int j = i; j < kBlock; ++j) x[to++] = dot4(kw[i], qw[j]);
         }
         fold(x, x8, 16);
         fold(x8, x4, 8);
@@ -154,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
     const int e = unit / p.H, h = unit - e * p.H;
     const int req = io.req_idx[e], slot = io.slot_idx[e];
     if (req < 0 || req >= p.R || slot < 0 || slot >= p.S) {
+        wait_previous_grid();
         if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
         return;
     }
@@ -164,7 +189,10 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
         len = 0;
     }
     const bool fresh = io.span.is_fresh(e);
-    if (len == 0 && !fresh) return;
+    if (len == 0 && !fresh) {
+        wait_previous_grid();
+        return;
+    }
     const long long first = io.span.seq_start[e];
     const int lane = threadIdx.x & 31, r = lane % RP;
     const int col = threadIdx.x / RP * kCols;  // of the CTA's
@@ -174,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, RP == 8 ? 2 : 3) prompt_tokens_kerne
     Incoming<RP, TYPE> in;
     in.load(io, p.H, h, col0, first, min(len, kTokens));
     in.store(st[0]);
+    wait_previous_grid();  // the states that are there already
 
     // x[b][c][0..1]: rows 4 (r + RP b) + {0, 1} and {2, 3} of column c
     float2 x[kBlocks][kCols][2];
@@ -313,6 +342,9 @@ template <int RP, int TYPE>
 cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
     const unsigned ctas = static_cast<unsigned>(io.n) * p.H * (kD / kCtaCols<RP>);
+    // begun while the states are unpacked, few CTAs save 1 to 2 us (16 of them: 21 against 22 us); many then crowd on some
+    // SMs (128: 47 against 39 us)
+    if (ctas <= 64) return launch_behind(prompt_tokens_kernel<RP, TYPE>, dim3(ctas), kThreads, 0, stream, p, io);
     prompt_tokens_kernel<RP, TYPE><<<ctas, kThreads, 0, stream>>>(p, io);
     count_launch();
     return cudaGetLastError();
@@ -331,7 +363,7 @@ cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t st
 {
     // 16-bit rows (that a tensor map can describe) go in chunks of 64 tokens; fewer tokens than that, whatever prompts they
     // are shared out into, are as fast or faster without (one prompt of 37 tokens on 4 heads 17 against 25 us, of 64 21 us
-    // both, of 80 25 against 23; 4 prompts of 16 tokens on 32 heads 25 against 34 us)
+    // both, of 80 25 against 23; 4 prompts of 15 tokens on 32 heads 25 against 34 us)
     const int total = io.span.total;
     if (io.dtype != STQ_F32 && p.H <= 65535 && total >= kPromptChunk && rows_mappable(io.q, p.H, total) && rows_mappable(io.k, p.H, total) &&
         rows_mappable(io.v, p.H, total))

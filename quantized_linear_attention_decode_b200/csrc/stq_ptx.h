@@ -167,15 +167,4 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, int dtype, float
     }
 }
 
-// Four of them.
-__device__ __forceinline__ float4 load4(const void *p, int64_t i, int dtype)
-{
-    if (dtype == STQ_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
-    if (dtype == STQ_BF16)
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
 }  // namespace stq
