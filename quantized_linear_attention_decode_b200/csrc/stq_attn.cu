@@ -307,6 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t pv = tc_idesc(type, kRows, kD, true);
             int queries = 0, tile = 0, done[2] = {0, 0};  // key tiles so far: of K and V, and of each query tile
             int keys[2] = {0, 0};
+            // elect.sync wants the whole warp, so lanes leave only by a verdict that all share: one for each tile of keys, behind its
+            // products (a vote for every wait, or products under a condition that lanes could differ in, cost 4 to 9 %).  After a
+            // wait that gave up, products go on until then, of whatever is there; no stage is handed back to the loads.
             const auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
                 if (elect_one()) {
                     uint32_t qa = smem_addr(sm.q[i]), ka = smem_addr(sm.k[(tile + j) % kStages]);
@@ -329,22 +332,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tiles[2] = {tiles_of(keys[0]), tiles_of(keys[1])}, all = max(tiles[0], tiles[1]), lk = value(3);
                 if (all == 0) continue;
                 ok = barrier_wait(smem_addr(&sm.q_full), queries++ & 1) && barrier_wait(smem_addr(&sm.k_full[tile % kStages]), tile / kStages & 1);
-                for (int i = 0; i < 2 && ok; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     if (tiles[i] == 0) continue;
-                    ok = free_scores(i);
-                    if (!ok) break;
+                    ok = ok && free_scores(i);
                     tc_fence_after();
                     scores(i, 0);
                 }
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (elect_one()) tc_commit(smem_addr(&sm.k_empty[tile % kStages]));
                 __syncwarp();
-                for (int j = 0; j < all && ok; ++j) {
+                for (int j = 0; j < all; ++j) {
                     const int s = (tile + j) % kStages, next = tile + j + 1;
-                    ok = barrier_wait(smem_addr(&sm.v_full[s]), (tile + j) / kStages & 1) &&
+                    ok = ok && barrier_wait(smem_addr(&sm.v_full[s]), (tile + j) / kStages & 1) &&
                          (j + 1 == all || barrier_wait(smem_addr(&sm.k_full[next % kStages]), next / kStages & 1));
-                    if (!ok) break;
                     if (j + 1 == all) {  // no more scores of these queries
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
                         if (elect_one()) tc_commit(smem_addr(&sm.q_empty));
                         __syncwarp();
                     }
@@ -358,12 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                     }
-                    for (int i = 0; i < 2 && ok; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         if (j >= tiles[i]) continue;
                         const bool first_half = is_short(keys[i], j);
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = barrier_wait(smem_addr(&sm.p_full[i][half]), done[i] & 1);
-                            if (!ok) break;
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && barrier_wait(smem_addr(&sm.p_full[i][half]), done[i] & 1);
                             tc_fence_after();
                             if (elect_one()) {
                                 uint32_t va = smem_addr(sm.v[s]);
@@ -376,16 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             __syncwarp();
                         }
-                        if (!ok) break;
                         ++done[i];
                         if (j + 1 < tiles[i]) {  // the next scores go where P is
-                            ok = free_scores(i);
-                            if (!ok) break;
+                            ok = ok && free_scores(i);
                             tc_fence_after();
                             scores(i, j + 1);
                         }
                     }
-                    if (ok && elect_one()) {
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (elect_one()) {
                         tc_commit(smem_addr(&sm.v_empty[s]));
                         if (j + 1 < all) tc_commit(smem_addr(&sm.k_empty[next % kStages]));
                     }

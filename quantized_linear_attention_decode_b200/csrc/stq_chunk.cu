@@ -548,11 +548,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll
             for (int pass = 0; pass < 2; ++pass) rt[pass] = prep[static_cast<size_t>(c) * H].r[32 * pass + lane];
             ok = barrier_wait(smem_addr(&sm.kq_raw), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.kq_empty), (c & 1) ^ 1));
-            if (!ok) break;
             // a lane's two tokens, 32 dims of each a warp; rows behind the prompt's last are not its own
             const uint8_t *rk = sm.raw_k[fw >> 1], *rq = sm.raw_q[fw >> 1];
 #pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
+            for (int pass = 0; pass < 2 && ok; ++pass) {
                 const int t = 32 * pass + lane;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -569,13 +568,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     *reinterpret_cast<float4 *>(sm.kq + kC * 128 + to1) = make_float4(tf32_hi(q2.x * r), tf32_hi(q2.y * r), tf32_hi(q3.x * r), tf32_hi(q3.y * r));
                 }
             }
-            fence_async_smem();
-            barrier_arrive(smem_addr(&sm.kq_full));
-            // K^T from the same
-            if (c > 0) ok = barrier_wait(smem_addr(&sm.kt_empty), (c & 1) ^ 1);
-            if (!ok) break;
+            if (ok) {
+                fence_async_smem();
+                barrier_arrive(smem_addr(&sm.kq_full));
+                // K^T from the same
+                if (c > 0) ok = barrier_wait(smem_addr(&sm.kt_empty), (c & 1) ^ 1);
+            }
 #pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
+            for (int pass = 0; pass < 2 && ok; ++pass) {
                 const int t = 32 * pass + lane;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -590,10 +590,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     }
                 }
             }
-            fence_async_smem();
-            barrier_arrive(smem_addr(&sm.kt_full));
-            asm volatile("bar.sync 2, 128;" ::: "memory");  // all have read what comes next over it
-            if (ft == 0 && c + 1 < chunks) fetch(c + 1);
+            if (ok) {
+                fence_async_smem();
+                barrier_arrive(smem_addr(&sm.kt_full));
+            }
+            ok = all_agree<2, kFeedThreads>(ok);  // all have read what comes next over it
+            if (ok && ft == 0 && c + 1 < chunks) fetch(c + 1);
         }
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -620,13 +622,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 fetch_v(0);
                 fetch_tp(0);
             }
-            asm volatile("bar.sync 1, 64;" ::: "memory");
-            for (int c = 0; c < chunks && ok; ++c) {
-                ok = barrier_wait(smem_addr(&sm.tp_raw_full), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1));
-                if (!ok) break;
+            all_agree<1, kSideThreads>(true);
+            for (int c = 0; c < chunks; ++c) {
+                // (ok may be false in the thread that fetches: the others learn it below)
+                ok = ok && barrier_wait(smem_addr(&sm.tp_raw_full), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1));
                 // ten blocks each of T and P, ten vectors a thread
 #pragma unroll
-                for (int i = 0; i < 10; ++i) {
+                for (int i = 0; i < 10 && ok; ++i) {
                     const int x = ft + kSideThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
                     const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
                     const int row = 16 * bi + in / 16, col = 16 * bj + in % 16;
@@ -637,9 +639,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     *reinterpret_cast<float4 *>(sm.t + kC * 128 + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
                     *reinterpret_cast<float4 *>(sm.p + swizzled(kC, row, col)) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
                 }
-                fence_async_smem();
-                barrier_arrive(smem_addr(&sm.tp_full));
-                asm volatile("bar.sync 1, 64;" ::: "memory");  // all have read what comes next over it
+                if (ok) {
+                    fence_async_smem();
+                    barrier_arrive(smem_addr(&sm.tp_full));
+                }
+                ok = all_agree<1, kSideThreads>(ok);  // all have read what comes next over it
+                if (!ok) break;
                 if (ft == 0 && c + 1 < chunks) {
                     fetch_tp(c + 1);
                     ok = barrier_wait(smem_addr(&sm.v_empty), c & 1);
@@ -652,6 +657,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             const uint32_t kq = smem_addr(sm.kq), kt = smem_addr(sm.kt), tt = smem_addr(sm.t), p = smem_addr(sm.p);
             // step s of 8 in an operand of blocks of 32 columns and `rows` rows
             const auto step = [](uint32_t base, int rows, int s) { return tc_desc(base + (s >> 2) * rows * 128 + (s & 3) * 32, 16, 1024); };
+            // (after a wait that gave up, products go on, of whatever is there, until all lanes have agreed on it, once a chunk:
+            // elect.sync wants the whole warp)
             for (int c = 0; c < chunks && ok; ++c) {
                 const uint32_t phase = c & 1;
                 // key rows 0-31 and 64-95 of X_0 come first
@@ -659,7 +666,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     ok = ok && barrier_wait(smem_addr(&sm.x_full[b]), phase);
-                    if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -679,9 +685,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     }
                     __syncwarp();
                 }
-                if (!ok) break;
-                ok = barrier_wait(smem_addr(&sm.tp_full), phase) && barrier_wait(smem_addr(&sm.r_full), phase);
-                if (!ok) break;
+                ok = ok && barrier_wait(smem_addr(&sm.tp_full), phase) && barrier_wait(smem_addr(&sm.r_full), phase);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -691,8 +695,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     tc_commit(smem_addr(&sm.u_done));
                 }
                 __syncwarp();
-                ok = barrier_wait(smem_addr(&sm.kt_full), phase) && barrier_wait(smem_addr(&sm.u_full), phase);
-                if (!ok) break;
+                ok = ok && barrier_wait(smem_addr(&sm.kt_full), phase) && barrier_wait(smem_addr(&sm.u_full), phase);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     tc_commit(smem_addr(&sm.y_done));
                     tc_commit(smem_addr(&sm.tp_empty));
                 }
-                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
             }
             if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
                 barrier_init(smem_addr(&sm.item), 1);

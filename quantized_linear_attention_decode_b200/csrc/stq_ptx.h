@@ -59,6 +59,22 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity)
     return true;
 }
 
+// Named barrier ID of `THREADS` threads (whole warps), at which all learn whether `ok` holds in every one of them: where
+// bounded waits lie between two such meetings, those that gave up still come to the next one.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool all_agree(bool ok)
+{
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(ok ? 1u : 0u), "n"(ID), "n"(THREADS)
+        : "memory");
+    return all != 0;
+}
+
 __device__ __forceinline__ void fence_barrier_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
