@@ -396,7 +396,7 @@ struct __align__(1024) ChunkSmem {
         float r[kC], d[kC];
     } rd[2];
     unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, tp_full, tp_empty, v_full, v_empty;
-    unsigned long long x_full[2], k_done, r_full, u_done, u_full, y_done, x_done;
+    unsigned long long x_full[2], k_done, r_full, u_done, u_full, y_done, x_done, drained;
     uint32_t tmem;
     int item[4];
 };
@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             init(sm.u_full, kGroupThreads);
             init(sm.y_done, 1);
             init(sm.x_done, 1);
+            init(sm.drained, 1);
             fence_barrier_init();
         }
         __syncwarp();
@@ -710,9 +711,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 ok = __all_sync(0xffffffffu, ok);
             }
             if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
-                barrier_init(smem_addr(&sm.item), 1);
-                tc_commit(smem_addr(&sm.item));
-                barrier_wait(smem_addr(&sm.item), 0);
+                tc_commit(smem_addr(&sm.drained));
+                barrier_wait(smem_addr(&sm.drained), 0);
             }
             __syncwarp();
         }

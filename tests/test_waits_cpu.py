@@ -33,3 +33,15 @@ def test_a_warp_that_issues_products_gives_up_as_one(path):
     assert any("__all_sync(" in line for line in lines)
     for before, line in zip(lines, lines[1:]):
         assert "break;" not in line or "__all_sync(" in before or (line == "if (!ok) break;" and before == "}"), line
+
+
+@pytest.mark.parametrize("path", [p for p in sorted(glob.glob(os.path.join(CSRC, "*.cu"))) if "barrier_init(" in open(p).read()],
+                         ids=os.path.basename)
+def test_barriers_are_64_bit_words(path):
+    """An mbarrier is a 64-bit word on its own boundary: a word declared as one, and nothing that another purpose laid down."""
+    code = _code(path)
+    words = {re.match(r"\w+", name.strip()).group() for names in re.findall(r"unsigned long long ([^;()=]+);", code) for name in names.split(",")}
+    code = re.sub(r"const auto init = [^\n]*", "", code)  # takes an unsigned long long &
+    used = re.findall(r"(?:barrier_init|barrier_wait|tc_commit)\(smem_addr\(&sm\.(\w+)", code) + re.findall(r"\binit\(sm\.(\w+)", code)
+    assert used or "bar0 = smem_addr(&sm.full[" in code
+    assert set(used) <= words
