@@ -35,15 +35,18 @@
  *     returns STQ_ERR_INDEX.  The decode still runs (its results stay
  *     undefined); the check costs a memset and a launch per call.
  *   - Setting the environment variable STQ_FAULT=alloc makes
- *     stq_pool_create fail with STQ_ERR_OOM, STQ_FAULT=launch makes every
- *     launching call fail with STQ_ERR_CUDA, both before any CUDA call
- *     (host-side fault injection for tests).  STQ_FAULT=timeout exercises the
- *     decode kernel's bounded waits: calls made while it is set shorten the
- *     wait limit from 1 s to 2 ms and make the first stage of the first CTA
- *     expect 16 bytes more than its copies deliver, so that every copy lands
- *     and that wait runs out; the kernel then waits (bounded) for its copies,
- *     returns, and stq_pool_check reports STQ_ERR_TIMEOUT.  The step's
- *     results are then undefined for the tiles that CTA did not finish.
+ *     stq_pool_create and stq_cache_create fail with STQ_ERR_OOM,
+ *     STQ_FAULT=launch makes every launching call fail with STQ_ERR_CUDA, both
+ *     before any CUDA call (host-side fault injection for tests).
+ *     STQ_FAULT=timeout exercises the bounded waits of the decode kernel and of
+ *     the kernels of 16-bit prompts (in chunks), prompt attention and cache
+ *     attention: calls made while it is set shorten the wait limit from 1 s to
+ *     2 ms and make the first stage of the first CTA (of the first warp, in
+ *     cache attention) expect 16 bytes more than its copies deliver, so that
+ *     every copy lands and that wait runs out; the kernel then waits (bounded)
+ *     for its copies, returns, and stq_pool_check (stq_cache_check, the err word)
+ *     reports STQ_ERR_TIMEOUT.  The call's results are then undefined for the
+ *     tiles that CTA did not finish.
  */
 #ifndef STQ_H
 #define STQ_H

@@ -187,10 +187,7 @@ stq::PoolView view(stq_pool *p)
     v.n_pivot_heads = p->n_pivot_heads;
     v.t = p->t;
     v.err = p->d_err;
-    // STQ_FAULT=timeout: a wait that nothing completes, given a short limit
-    const bool stall = fault("timeout");
-    v.wait_ns = stall ? 2000000ull : 1000000000ull;
-    v.stall_tx = stall ? 16u : 0u;
+    v.waits = stq::waits();
     return v;
 }
 

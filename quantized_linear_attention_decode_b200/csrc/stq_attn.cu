@@ -64,6 +64,7 @@ struct PromptAttn {
     bool negative;     // scale < 0
     void *y;
     int32_t *err;
+    Waits waits;
 };
 
 struct __align__(1024) AttnSmem {
@@ -176,10 +177,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_tile = kRows / a.pack;  // tokens of a query tile
     bool ok = true;
 
+    const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, a.waits.ns); };
     // Item n of this CTA, a value a lane; false: no more.  The whole warp calls these.
     int entry = 0;
     const auto take = [&](int n) {
-        ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.item_full[n & 1]), n >> 1 & 1));
+        ok = __all_sync(0xffffffffu, wait(sm.item_full[n & 1], n >> 1 & 1));
         if (ok) entry = sm.item[n & 1][lane & 7];
         return ok && __shfl_sync(0xffffffffu, entry, 0) >= 0;
     };
@@ -226,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     ++n;
                     // not before this one's loads are under way, so that no CTA keeps an item waiting that another could run
-                    ok = barrier_wait(smem_addr(&sm.wanted), (n - 1) & 1) &&
-                         (n < 2 || barrier_wait(smem_addr(&sm.item_empty[n & 1]), (n >> 1 & 1) ^ 1));
+                    ok = wait(sm.wanted, (n - 1) & 1) &&
+                         (n < 2 || wait(sm.item_empty[n & 1], (n >> 1 & 1) ^ 1));
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     next_block(smem_addr(&sm.answer), smem_addr(&sm.asked));
                 }
                 __syncwarp();
-                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.asked), asked & 1));
+                ok = __all_sync(0xffffffffu, wait(sm.asked, asked & 1));
                 if (!ok) break;
                 ++asked;
                 const bool more = next_block_is(smem_addr(&sm.answer), &x);
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int q_row = value(0) + value(4), k_row = value(2), block = value(5), kv_head = block / (a.group / a.pack);
                 if (lane == 0 && all > 0) {
                     const uint32_t qf = smem_addr(&sm.q_full);
-                    ok = queries == 0 || barrier_wait(smem_addr(&sm.q_empty), (queries & 1) ^ 1);
+                    ok = queries == 0 || wait(sm.q_empty, (queries & 1) ^ 1);
                     if (ok) {
                         barrier_expect(qf, (tiles[0] > 0 ? kTileBytes : 0) + (tiles[1] > 0 ? kTileBytes : 0));
                         for (int i = 0; i < 2; ++i)
@@ -273,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int s = tile % kStages;
                         const uint32_t parity = (tile / kStages & 1) ^ 1;
                         const uint32_t kf = smem_addr(&sm.k_full[s]), vf = smem_addr(&sm.v_full[s]);
-                        ok = tile < kStages || barrier_wait(smem_addr(&sm.k_empty[s]), parity);
+                        ok = tile < kStages || wait(sm.k_empty[s], parity);
                         if (!ok) break;
-                        barrier_expect(kf, kTileBytes);
+                        barrier_expect(kf, kTileBytes + (tile == 0 && blockIdx.x == 0 ? a.waits.stall_tx : 0));
                         for (int half = 0; half < 2; ++half)
                             tma_load3(smem_addr(sm.k[s]) + half * kHalfTile, &k_map, kf, 64 * half, kv_head, k_row + j * kRows);
-                        ok = tile < kStages || barrier_wait(smem_addr(&sm.v_empty[s]), parity);
+                        ok = tile < kStages || wait(sm.v_empty[s], parity);
                         barrier_expect(vf, kTileBytes);
                         for (int half = 0; half < 2; ++half)
                             tma_load3(smem_addr(sm.v[s]) + half * kHalfTile, &v_map, vf, 64 * half, kv_head, k_row + j * kRows);
@@ -291,10 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 taken(n);
             }
             if (!ok && lane == 0) {  // the loads in flight land before the memory is given back
-                if (queries > 0) barrier_wait(smem_addr(&sm.q_full), (queries - 1) & 1);
+                if (queries > 0) wait(sm.q_full, (queries - 1) & 1);
                 for (int j = max(0, tile - kStages); j < tile; ++j) {
-                    barrier_wait(smem_addr(&sm.k_full[j % kStages]), j / kStages & 1);
-                    barrier_wait(smem_addr(&sm.v_full[j % kStages]), j / kStages & 1);
+                    wait(sm.k_full[j % kStages], j / kStages & 1);
+                    wait(sm.v_full[j % kStages], j / kStages & 1);
                 }
             }
             __syncwarp();
@@ -324,14 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
             // S_i may be written over: the product that reads P in its place is done
-            const auto free_scores = [&](int i) { return done[i] == 0 || barrier_wait(smem_addr(&sm.o_full[i]), (done[i] - 1) & 1); };
+            const auto free_scores = [&](int i) { return done[i] == 0 || wait(sm.o_full[i], (done[i] - 1) & 1); };
             for (int n = 0; take(n); ++n) {
                 taken(n);
                 keys[0] = keys_of(0);
                 keys[1] = keys_of(1);
                 const int tiles[2] = {tiles_of(keys[0]), tiles_of(keys[1])}, all = max(tiles[0], tiles[1]), lk = value(3);
                 if (all == 0) continue;
-                ok = barrier_wait(smem_addr(&sm.q_full), queries++ & 1) && barrier_wait(smem_addr(&sm.k_full[tile % kStages]), tile / kStages & 1);
+                ok = wait(sm.q_full, queries++ & 1) && wait(sm.k_full[tile % kStages], tile / kStages & 1);
                 for (int i = 0; i < 2; ++i) {
                     if (tiles[i] == 0) continue;
                     ok = ok && free_scores(i);
@@ -344,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 for (int j = 0; j < all; ++j) {
                     const int s = (tile + j) % kStages, next = tile + j + 1;
-                    ok = ok && barrier_wait(smem_addr(&sm.v_full[s]), (tile + j) / kStages & 1) &&
-                         (j + 1 == all || barrier_wait(smem_addr(&sm.k_full[next % kStages]), next / kStages & 1));
+                    ok = ok && wait(sm.v_full[s], (tile + j) / kStages & 1) &&
+                         (j + 1 == all || wait(sm.k_full[next % kStages], next / kStages & 1));
                     if (j + 1 == all) {  // no more scores of these queries
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j >= tiles[i]) continue;
                         const bool first_half = is_short(keys[i], j);
                         for (int half = 0; half < 2; ++half) {
-                            ok = ok && barrier_wait(smem_addr(&sm.p_full[i][half]), done[i] & 1);
+                            ok = ok && wait(sm.p_full[i][half], done[i] & 1);
                             tc_fence_after();
                             if (elect_one()) {
                                 uint32_t va = smem_addr(sm.v[s]);
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
                 tc_commit(smem_addr(&sm.drained));
-                barrier_wait(smem_addr(&sm.drained), 0);
+                wait(sm.drained, 0);
             }
             __syncwarp();
         }
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int least = min(value(3), value(4) + i * per_tile + value(3) - value(1) + 1);  // that the tile's first row sees
             float top = -INFINITY, sum = 0.0f;  // in units of log 2: P = exp2(c s - top)
             for (int j = 0; j < tiles && ok; ++j, ++done) {
-                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.s_full[i]), done & 1));
+                ok = __all_sync(0xffffffffu, wait(sm.s_full[i], done & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const bool first_half = is_short(keys, j);
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
             }
-            if (ok && tiles > 0) ok = barrier_wait(smem_addr(&sm.o_full[i]), (done - 1) & 1);
+            if (ok && tiles > 0) ok = wait(sm.o_full[i], (done - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -590,6 +592,7 @@ extern "C" stq_status stq_attn_prompt(const int32_t *q_start, const int32_t *k_s
     a.negative = scale < 0.0f;
     a.y = y;
     a.err = err;
+    a.waits = stq::waits();
     const auto kernel = dtype == STQ_BF16 ? stq::attn_prompt_kernel<true> : stq::attn_prompt_kernel<false>;
     const int smem = static_cast<int>(sizeof(stq::AttnSmem)) + 1024;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

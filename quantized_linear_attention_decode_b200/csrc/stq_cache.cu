@@ -207,6 +207,7 @@ struct AttnArgs {
     float scale_log2;  // scale log2(e)
     void *y;
     float *part;
+    Waits waits;
 };
 
 // Floats of one partial: sums [8 NT][128], then R and the sum of weights of each head.
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel
             absent &= ~(1u << k);
             if (lane == 0) {
                 const uint32_t bytes = s.shift == 2 ? kHalfBlock : kUnitBytes;
-                barrier_expect(bar0 + 8 * k, bytes);
+                barrier_expect(bar0 + 8 * k, bytes + (me == 0 && issued == 0 ? a.waits.stall_tx : 0));
                 bulk_copy(st0 + k * kUnitBytes, a.c.block(id, head) + half * kHalfBlock, bytes, bar0 + 8 * k);
             }
         } else {
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel
         begin_segment(a, sg, w.seq, h0, nh);
         for (int u = u0; u < u1; ++u) {
             const int k = taken % kStagesW;
-            if (!__all_sync(0xffffffffu, barrier_wait(bar0 + 8 * k, taken / kStagesW & 1))) {
+            if (!__all_sync(0xffffffffu, barrier_wait(bar0 + 8 * k, taken / kStagesW & 1, a.waits.ns))) {
                 if (lane == 0) atomicOr(a.c.err, kErrTimeout);
                 dead = true;
                 break;
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel
     }
     // after a wait that gave up, let the copies in flight land (bounded) before the memory is given back
     if (dead)
-        for (; taken < issued; ++taken) barrier_wait(bar0 + 8 * (taken % kStagesW), taken / kStagesW & 1);
+        for (; taken < issued; ++taken) barrier_wait(bar0 + 8 * (taken % kStagesW), taken / kStagesW & 1, a.waits.ns);
 }
 
 // Joins the partial sums of one (sequence, query head) in the order of the warps
@@ -968,6 +969,7 @@ stq_status stq_attn_decode(stq_cache *c, const int32_t *page_table, int32_t max_
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.y = y;
     a.part = static_cast<float *>(workspace);
+    a.waits = stq::waits();
     a.warps = stq::attn_warps(c, nt);
     const cudaError_t e = nt == 2 ? stq::launch_attn<2>(a, static_cast<cudaStream_t>(stream))
                                   : stq::launch_attn<1>(a, static_cast<cudaStream_t>(stream));

@@ -522,12 +522,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     wait_previous_grid();  // T and P, and the states that are there already
     const Prepared *prep = prepared(io, H, e, 0, h);
     bool ok = true;
+    const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, pool.waits.ns); };
     // after a wait that gave up: loads in flight land before the memory is given back (no more than one phase each is)
     const auto drain = [&] {
         if (tid == kGroupThreads || tid == kGroupThreads + kFeedThreads + 32)
-            for (const auto *bar : {&sm.kq_raw, &sm.tp_raw_full, &sm.v_full}) {
-                barrier_wait(smem_addr(bar), 0);
-                barrier_wait(smem_addr(bar), 1);
+            for (auto *bar : {&sm.kq_raw, &sm.tp_raw_full, &sm.v_full}) {
+                wait(*bar, 0);
+                wait(*bar, 1);
             }
     };
 
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const int ft = tid - kGroupThreads, fw = warp - 8;
         const auto fetch = [&](int c) {  // as they are, by one thread
             const uint32_t bar = smem_addr(&sm.kq_raw);
-            barrier_expect(bar, 4 * kC * 128);
+            barrier_expect(bar, 4 * kC * 128 + (c == 0 && blockIdx.x == 0 ? pool.waits.stall_tx : 0));
             for (int half = 0; half < 2; ++half) {
                 tma_load3(smem_addr(sm.raw_k[half]), &k_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
                 tma_load3(smem_addr(sm.raw_q[half]), &q_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             float rt[2];
 #pragma unroll
             for (int pass = 0; pass < 2; ++pass) rt[pass] = prep[static_cast<size_t>(c) * H].r[32 * pass + lane];
-            ok = barrier_wait(smem_addr(&sm.kq_raw), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.kq_empty), (c & 1) ^ 1));
+            ok = wait(sm.kq_raw, c & 1) && (c == 0 || wait(sm.kq_empty, (c & 1) ^ 1));
             // a lane's two tokens, 32 dims of each a warp; rows behind the prompt's last are not its own
             const uint8_t *rk = sm.raw_k[fw >> 1], *rq = sm.raw_q[fw >> 1];
 #pragma unroll
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 fence_async_smem();
                 barrier_arrive(smem_addr(&sm.kq_full));
                 // K^T from the same
-                if (c > 0) ok = barrier_wait(smem_addr(&sm.kt_empty), (c & 1) ^ 1);
+                if (c > 0) ok = wait(sm.kt_empty, (c & 1) ^ 1);
             }
 #pragma unroll
             for (int pass = 0; pass < 2 && ok; ++pass) {
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             all_agree<1, kSideThreads>(true);
             for (int c = 0; c < chunks; ++c) {
                 // (ok may be false in the thread that fetches: the others learn it below)
-                ok = ok && barrier_wait(smem_addr(&sm.tp_raw_full), c & 1) && (c == 0 || barrier_wait(smem_addr(&sm.tp_empty), (c & 1) ^ 1));
+                ok = ok && wait(sm.tp_raw_full, c & 1) && (c == 0 || wait(sm.tp_empty, (c & 1) ^ 1));
                 // ten blocks each of T and P, ten vectors a thread
 #pragma unroll
                 for (int i = 0; i < 10 && ok; ++i) {
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 if (!ok) break;
                 if (ft == 0 && c + 1 < chunks) {
                     fetch_tp(c + 1);
-                    ok = barrier_wait(smem_addr(&sm.v_empty), c & 1);
+                    ok = wait(sm.v_empty, c & 1);
                     if (ok) fetch_v(c + 1);
                 }
             }
@@ -663,10 +664,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int c = 0; c < chunks && ok; ++c) {
                 const uint32_t phase = c & 1;
                 // key rows 0-31 and 64-95 of X_0 come first
-                ok = barrier_wait(smem_addr(&sm.kq_full), phase);
+                ok = wait(sm.kq_full, phase);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    ok = ok && barrier_wait(smem_addr(&sm.x_full[b]), phase);
+                    ok = ok && wait(sm.x_full[b], phase);
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     }
                     __syncwarp();
                 }
-                ok = ok && barrier_wait(smem_addr(&sm.tp_full), phase) && barrier_wait(smem_addr(&sm.r_full), phase);
+                ok = ok && wait(sm.tp_full, phase) && wait(sm.r_full, phase);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -696,7 +697,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     tc_commit(smem_addr(&sm.u_done));
                 }
                 __syncwarp();
-                ok = ok && barrier_wait(smem_addr(&sm.kt_full), phase) && barrier_wait(smem_addr(&sm.u_full), phase);
+                ok = ok && wait(sm.kt_full, phase) && wait(sm.u_full, phase);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             }
             if (!ok && elect_one()) {  // products in flight end (bounded) before the memory is given back
                 tc_commit(smem_addr(&sm.drained));
-                barrier_wait(smem_addr(&sm.drained), 0);
+                wait(sm.drained, 0);
             }
             __syncwarp();
         }
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int i = 0; i < 32; i += 2) put_pair(x + i, __fmul2_rn(pair_at(x + i), make_float2(x_next, x_next)));
             tmem_store32(base + kColX + col, x);
         };
-        ok = barrier_wait(smem_addr(&sm.v_full), 0);
+        ok = wait(sm.v_full, 0);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             const float x_next = sm.rd[0].r[kC - 1];
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 vs[i] = widen1<BF16>(*reinterpret_cast<const uint16_t *>(v + 128 * t + (((j >> 3 & 7) ^ (t & 7)) << 4)));
             }
             barrier_arrive(smem_addr(&sm.v_empty));
-            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.k_done), phase));
+            ok = __all_sync(0xffffffffu, wait(sm.k_done, phase));
             if (!ok) break;
             tc_fence_after();
             tmem_load32(base + kColK + 32 * half, x);
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tc_fence_before();
             barrier_arrive(smem_addr(&sm.r_full));
             // U, and D U
-            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.u_done), phase));
+            ok = __all_sync(0xffffffffu, wait(sm.u_done, phase));
             if (!ok) break;
             tc_fence_after();
             tmem_load32(base + kColHi + 32 * half, x);
@@ -838,11 +839,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             // the state after the chunk
             float x_next = 0.0f;
             if (c + 1 < chunks) {
-                ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.v_full), phase ^ 1));
+                ok = __all_sync(0xffffffffu, wait(sm.v_full, phase ^ 1));
                 if (!ok) break;
                 x_next = sm.rd[phase ^ 1].r[kC - 1];
             }
-            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.x_done), phase));
+            ok = __all_sync(0xffffffffu, wait(sm.x_done, phase));
             if (!ok) break;
             tc_fence_after();
             // the first half of this thread's rows, then Y (whose products come behind the state's; the next chunk's
@@ -859,7 +860,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 }
             };
             update(0);
-            ok = __all_sync(0xffffffffu, barrier_wait(smem_addr(&sm.y_done), phase));
+            ok = __all_sync(0xffffffffu, wait(sm.y_done, phase));
             if (!ok) break;
             tc_fence_after();
             tmem_load32(base + kColY + 32 * half, x);

@@ -24,6 +24,17 @@ inline bool fault(const char *which)
     return f != nullptr && std::strcmp(f, which) == 0;
 }
 
+// STQ_FAULT=timeout: a wait that nothing completes, given a short limit.
+inline Waits waits()
+{
+    Waits w;
+    if (fault("timeout")) {
+        w.ns = 2000000ull;
+        w.stall_tx = 16;
+    }
+    return w;
+}
+
 // An NVTX range over a launching call (a no-op unless a profiler is attached),
 // so that profiles attribute device work to the entry point that queued it.
 struct NvtxRange {

@@ -46,6 +46,12 @@ struct Tables {
     const int32_t *pivot_head;  // GDN: the FP16 pivot heads, ascending (n_pivot_heads of them)
 };
 
+// How long device-side waits last, and a test hook: bytes that the first barrier of a launch expects beyond its copies.
+struct Waits {
+    unsigned long long ns = 1000000000ull;  // limit of every bounded wait
+    uint32_t stall_tx = 0;
+};
+
 struct PoolView {
     uint8_t *pages;      // [R][S][slot_bytes]
     size_t slot_bytes;
@@ -60,8 +66,7 @@ struct PoolView {
     int n_pivot_heads;   // GDN: heads held in FP16 (their own kernel), listed in t.pivot_head
     Tables t;
     uint32_t *err;
-    unsigned long long wait_ns;  // limit of every bounded device-side wait
-    uint32_t stall_tx;           // test hook: bytes the first stage of CTA 0 expects beyond its copies
+    Waits waits;
 };
 
 struct DecodeIO {

@@ -19,8 +19,6 @@ __device__ __forceinline__ unsigned long long time_ns()
     return t;
 }
 
-constexpr unsigned long long kWaitNs = 1000000000ull;  // limit of every bounded wait: 1 s
-
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -49,13 +47,13 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Waits for the phase of parity `parity`; false when it has not come within kWaitNs.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity)
+// Waits for the phase of parity `parity`; false when it has not come within `limit` ns.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, unsigned long long limit)
 {
     if (barrier_try(bar, parity)) return true;
     const unsigned long long t0 = time_ns();
     while (!barrier_try(bar, parity))
-        if (time_ns() - t0 > kWaitNs) return false;
+        if (time_ns() - t0 > limit) return false;
     return true;
 }
 

@@ -41,7 +41,7 @@ def test_barriers_are_64_bit_words(path):
     """An mbarrier is a 64-bit word on its own boundary: a word declared as one, and nothing that another purpose laid down."""
     code = _code(path)
     words = {re.match(r"\w+", name.strip()).group() for names in re.findall(r"unsigned long long ([^;()=]+);", code) for name in names.split(",")}
-    code = re.sub(r"const auto init = [^\n]*", "", code)  # takes an unsigned long long &
-    used = re.findall(r"(?:barrier_init|barrier_wait|tc_commit)\(smem_addr\(&sm\.(\w+)", code) + re.findall(r"\binit\(sm\.(\w+)", code)
+    code = re.sub(r"const auto (init|wait) = [^\n]*", "", code)  # these take an unsigned long long &
+    used = [a or b for a, b in re.findall(r"(?:barrier_init|tc_commit|barrier_arrive)\(smem_addr\(&sm\.(\w+)|\bwait\(sm\.(\w+)", code)] + re.findall(r"\binit\(sm\.(\w+)", code)
     assert used or "bar0 = smem_addr(&sm.full[" in code
     assert set(used) <= words
