@@ -376,7 +376,8 @@ __device__ __forceinline__ void begin_segment(const AttnArgs &a, Segment<NT> &sg
         // the largest product gives the largest score
         const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 100);
         const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23), a.scale_log2);
-        const float f = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+        // (at least 2^-100, so that a hidden token's -inf stays one; sums of products are below 2^40, scores below 2^-60 then)
+        const float f = fmaxf(fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23), 0x1p-100f);
 #pragma unroll
         for (int gi = 0; gi < 4; ++gi) {
 #pragma unroll
