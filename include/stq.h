@@ -422,6 +422,11 @@ typedef struct {
  *              aligned, owned by the caller; its content need not be kept between
  *              calls.  Calls that may overlap on the GPU need one each, and a
  *              state each.
+ * A NaN in a token's q makes its y of that head NaN; one in its k, v, beta or alpha
+ * (or in the starting state) the state and y that depend on it, from that token on,
+ * and with 16-bit rows y of up to 63 tokens before it may be NaN too.  A state that
+ * is not finite is reported (STQ_ERR_NONFINITE); other heads and entries are not
+ * touched by it.
  * KDA pools (a decay for each key row) return STQ_ERR_UNSUPPORTED.
  */
 stq_status stq_prompt_workspace(const stq_pool *pool, int32_t n, int32_t total, size_t *bytes);

@@ -15,6 +15,10 @@
 // and enter the tensor core as two tf32 terms, x = hi + lo, 2^-21 of x left: 2 products
 // against k, 3 of the 4 for T times a vector.  Y is rounded to 16 bits: of R Q, P and U one
 // term each, rounded to nearest (2^-11).  Sums are fp32.
+//
+// What is no number stays none.  A NaN in q is one in its row of P; one in X_0, v or the decays is one in a whole column of
+// V - diag(R) K X_0 (products with zeros keep it), so of U, Y and X_C; one in k or b in rows of T, so in U.  So P and U
+// alone take care to keep it.  Y has it from the chunk's first token on, since P's zeros above the diagonal meet U's rows.
 #include <cmath>
 
 #include "stq_host.h"
@@ -44,8 +48,12 @@ __device__ __forceinline__ Prepared *prepared(const PromptIO &io, int H, int e, 
 
 __device__ __forceinline__ int block_of(int i, int j) { return (i * (i + 1) / 2 + j) * kBlockFloats; }
 
-// x rounded to tf32, to nearest; what is left of it.
+// x rounded to tf32, to nearest; what is left of it.  Arithmetic's NaN, 0x7fffffff, is carried over into minus zero: it lives on in
+// the rest, so where no rest follows something else has to keep it.
 __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
+
+// ... and a NaN kept (by cvt.rna.tf32 the walk took 8 % longer, at half as many places).
+__device__ __forceinline__ float tf32_hi_or_nan(float x) { return isnan(x) ? x : tf32_hi(x); }
 
 // The same by cutting, for a first term whose rest follows: what the tensor core cuts off the rest is 2^-21 of x.
 __device__ __forceinline__ float tf32_cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
             }
             const float beta = s.beta[t];
             const float2 a = make_float2(i < t ? beta * (r.x * kk[nt][2 * half]) : 0.0f, i + 1 < t ? beta * (r.y * kk[nt][2 * half + 1]) : 0.0f);
-            const float2 p = make_float2(i <= t ? tf32_hi(r.x * qk[nt][2 * half]) : 0.0f, i + 1 <= t ? tf32_hi(r.y * qk[nt][2 * half + 1]) : 0.0f);
+            const float2 p = make_float2(i <= t ? tf32_hi_or_nan(r.x * qk[nt][2 * half]) : 0.0f, i + 1 <= t ? tf32_hi_or_nan(r.y * qk[nt][2 * half + 1]) : 0.0f);
             *reinterpret_cast<float2 *>(&s.m.a[t][i]) = a;
             *reinterpret_cast<float2 *>(out->p + block_of(warp, nt / 2) + (t & 15) * 16 + (i & 15)) = p;
         }
@@ -823,6 +831,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int i = 0; i < 32; i += 2) put_pair(x + i, __fadd2_rn(pair_at(x + i), pair_at(w + i)));
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
+            // One NaN in a column of U makes its whole column of Y one, as it should be (below): zero times U is added to an element.
+            float2 none[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) none[i >> 1 & 1] = __ffma2_rn(pair_at(x + i), make_float2(0.0f, 0.0f), none[i >> 1 & 1]);
+            w[0] = __float_as_uint(__uint_as_float(w[0]) + ((none[0].x + none[0].y) + (none[1].x + none[1].y)));
             tmem_store32(base + kColK + 32 * half, w);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) put_pair(x + i, __fmul2_rn(pair_at(x + i), *reinterpret_cast<const float2 *>(&rd.d[32 * half + i])));

@@ -1,0 +1,74 @@
+"""GPU: stq_prompt_step at its edges."""
+import numpy as np
+import pytest
+
+from quantized_linear_attention_decode_b200 import stq
+from test_gpu_prompt import _Prompts, _cuda
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+KINDS = ["bf16", "fp16", "fp32"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_nan_in_q_is_in_its_row_of_y(kind):
+    s = _Prompts([200, 70], 3, kind, seed=51)
+    want_y, want = (t.clone() for t in s.run())
+    s.q[70, 1, 5] = float("nan")
+    y, state = s.run()
+    assert bool(y[70, 1].isnan().all())
+    assert torch.equal(state, want)
+    y[70, 1] = want_y[70, 1]
+    assert torch.equal(y, want_y)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", [0, 70, 199])
+def test_a_nan_in_v_is_in_its_column_from_there_on(kind, t):
+    s = _Prompts([200, 70], 3, kind, seed=52)
+    want_y, want = (x.clone() for x in s.run())
+    s.v[t, 1, 5] = float("nan")
+    y, state = s.run()
+    assert stq.stq_pool_check(s.pool, raise_on_error=False) == stq.STQ_ERR_NONFINITE
+    assert bool(y[t:200, 1, 5].isnan().all()) and bool(state[0, 1, :, 5].isnan().all())
+    # other columns, heads and prompts, and chunks of 64 that ended before
+    rest = torch.ones(270, 3, 128, dtype=torch.bool, device="cuda")
+    rest[t - t % 64:200, 1, 5] = False
+    assert torch.equal(y[rest], want_y[rest])
+    rest = torch.ones_like(state, dtype=torch.bool)
+    rest[0, 1, :, 5] = False
+    assert torch.equal(state[rest], want[rest])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name", ["k", "beta", "alpha"])
+def test_a_nan_in_k_and_the_gates_is_in_y_from_there_on(kind, name):
+    s = _Prompts([200, 70], 3, kind, seed=53)
+    want_y, want = (x.clone() for x in s.run())
+    x = getattr(s, name)
+    if name == "k":
+        x[70, 1, 5] = float("nan")
+    else:
+        x[70, 1] = float("nan")
+    y, state = s.run()
+    assert stq.stq_pool_check(s.pool, raise_on_error=False) == stq.STQ_ERR_NONFINITE
+    assert bool(y[70:200, 1].isnan().all()) and bool(state[0, 1].isnan().all())
+    assert torch.equal(y[:64], want_y[:64]) and torch.equal(y[200:], want_y[200:]) and torch.equal(state[1], want[1])
+    for h in (0, 2):
+        assert torch.equal(y[:, h], want_y[:, h]) and torch.equal(state[:, h], want[:, h])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_state_that_is_no_number_is_in_its_column(kind, bad):
+    """A page of an fp32 pool that an earlier call spoilt."""
+    s = _Prompts([200], 2, kind, seed=54, bits=32, fresh=[0])
+    S = _cuda(s.S0.astype(np.float32))
+    S[0, 1, 7, 5] = bad
+    stq.stq_quantize_state(s.pool, s.req, s.slot, S)
+    stq.stq_pool_check(s.pool, raise_on_error=False)
+    y, state = s.run()
+    assert not bool(y[:, 1, 5].isfinite().any())
+    keep = torch.arange(128, device="cuda") != 5
+    assert bool(y[:, 0].isfinite().all()) and bool(y[:, 1, keep].isfinite().all())
