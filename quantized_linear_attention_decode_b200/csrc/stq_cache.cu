@@ -473,12 +473,13 @@ __device__ __forceinline__ void take_unit(Segment<NT> &sg, const uint8_t *b, int
                 for (int j = 0; j < 4; ++j)
                     if ((m0 + mt) * 16 + g + (j >> 1) * 8 >= valid) x[mt][nt][j] = -INFINITY;
     }
-    // the largest value scale (positive binary16 values order as integers), as a power of two >= 1
+    // the largest value scale of the sequence's tokens (positive binary16 values order as integers), as a power of two >= 1
     uint32_t mu = 0;
 #pragma unroll
     for (int half = 0; half < (MT + 1) / 2; ++half) {
         const uint2 vs = *reinterpret_cast<const uint2 *>(b + half * kHalfBlock + kValueScales + 8 * lane);
-        mu = __vmaxu2(mu, __vmaxu2(vs.x, vs.y));
+        const int there = valid - half * kHalf - (lane & 30);  // of this lane's two tokens: what a page's last user left says nothing
+        mu = __vmaxu2(mu, __vmaxu2(vs.x, vs.y) & (there >= 2 ? 0xffffffffu : there == 1 ? 0xffffu : 0u));
     }
     const uint32_t biggest = __reduce_max_sync(0xffffffffu, max(mu & 0xffffu, mu >> 16));
     const float up = static_cast<float>(max(0, static_cast<int>(biggest >> 10) - 14));

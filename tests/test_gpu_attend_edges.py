@@ -1,7 +1,9 @@
 """GPU: attention of single tokens over the 4-bit cache at its edges."""
+import numpy as np
 import pytest
 
-from test_gpu_cache import _Sequences
+from quantized_linear_attention_decode_b200 import stq
+from test_gpu_cache import _Sequences, _cuda
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -31,3 +33,19 @@ def test_queries_of_zeros_and_near_them(lens, scale):
     y = s.attend(scale=scale)
     assert bool(y.isfinite().all())
     s.check(y, 128 ** -0.5 if scale is None else scale)
+
+
+@pytest.mark.parametrize("lens", [[70, 1, 127], [17, 33], [5], [64 * 40 + 2] * 3])
+@pytest.mark.parametrize("size", [0.02, 1.0])
+def test_recycled_pages_give_the_bits_of_new_ones(lens, size):
+    """Tokens behind a sequence's end, left by another sequence with values near the top of binary16."""
+    s = _Sequences(lens, 8, 2, "bf16", seed=33, size=size)
+    s.append()
+    y = s.attend()
+    assert bool(y.isfinite().all())
+    s.check(y)
+    stale = np.concatenate([s.table[i, -(-m // 64) - 1].astype(np.int64) * 64 + np.arange(m % 64, 64) for i, m in enumerate(s.lens)])
+    big = torch.randn(len(stale), 2, 128, device="cuda") * 1e5
+    stq.stq_cache_append(s.cache, _cuda(stale), big, big)
+    stq.stq_cache_check(s.cache, raise_on_error=False)  # (groups above binary16's range are reported, and zero)
+    assert torch.equal(s.attend(), y)
