@@ -29,7 +29,9 @@
 // The running maximum that P is taken against moves only when a score lies more than
 // 2^8 above it (P then stays below 2^8, within fp16's range), so O is rescaled in
 // tensor memory a few times a row and not in every tile.  P is rounded to the type of
-// v (2^-9 of a weight in bf16, as the output itself); all else is fp32.
+// v (2^-9 of a weight in bf16, as the output itself); all else is fp32.  In fp16 P and
+// its sum are lifted by 2^7, as far as that range allows: weights down to 2^-21 of the
+// largest keep their bits, and what is lost of smaller ones is 2^-32 of it.
 //
 // A tile's products take 1090 cycles (S reads both operands from shared memory, 72
 // cycles a step of 16 against 64 of arithmetic), and the next scores wait 300 more for
@@ -56,6 +58,9 @@ constexpr int kStages = 2;
 constexpr int kThreads = 384;  // three warpgroups; warp 10 finds the items, warp 11 only hands its registers over
 // registers a thread: 168 at launch, then 208 in the softmax warpgroups and 88 in the third (2 * 208 + 88 = 3 * 168)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;  // log2 of what P is multiplied by
 
 struct PromptAttn {
     const int32_t *q_start, *k_start;
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int keys = keys_of(i), tiles = tiles_of(keys);
             const int sees = min(value(3), value(4) + i * per_tile + row / a.pack + value(3) - value(1) + 1);  // keys that this row sees (none: <= 0)
             const int least = min(value(3), value(4) + i * per_tile + value(3) - value(1) + 1);  // that the tile's first row sees
-            float top = -INFINITY, sum = 0.0f;  // in units of log 2: P = exp2(c s - top)
+            float top = -INFINITY, sum = 0.0f;  // in units of log 2: P = exp2(c s - top + kLift)
             for (int j = 0; j < tiles && ok; ++j, ++done) {
                 ok = __all_sync(0xffffffffu, wait(sm.s_full[i], done & 1));
                 if (!ok) break;
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                const float off = top == -INFINITY ? 0.0f : -top;
+                const float off = top == -INFINITY ? 0.0f : kLift<BF16> - top;
                 float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
