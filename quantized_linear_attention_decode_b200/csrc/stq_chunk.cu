@@ -38,11 +38,16 @@ struct Prepared {
 };
 static_assert(sizeof(Prepared) == kPreparedBytes, "workspace size");
 
-// Where chunk `at` of entry e has its Prepared: distinct for ranges that do not overlap, and within
-// prompt_chunks(n, total) for any range within [0, total].
-__device__ __forceinline__ Prepared *prepared(const PromptIO &io, int H, int e, int at, int h)
+// Chunks are numbered through all entries in their order, whatever rows these have: there are no more than
+// prompt_chunks(n, total) where ranges do not overlap.
+__device__ __forceinline__ int chunks_of(const PromptIO &io, int e)
 {
-    const long long chunk = io.span.seq_start[e] / kC + e + at;
+    const int len = io.span.length(e);
+    return len > 0 ? (len + kC - 1) / kC : 0;
+}
+
+__device__ __forceinline__ Prepared *prepared(const PromptIO &io, int H, long long chunk, int h)
+{
     return reinterpret_cast<Prepared *>(io.workspace) + chunk * H + h;
 }
 
@@ -124,10 +129,9 @@ struct PrepSmem {
 __device__ __forceinline__ bool find_chunk(const PromptIO &io, int chunk, int *entry, int *at)
 {
     const int lane = threadIdx.x & 31;
-    int base = 0;
+    long long base = 0;
     for (int first = 0; first < io.n; first += 32) {
-        const int len = first + lane < io.n ? io.span.length(first + lane) : 0;
-        const int mine = len > 0 ? (len + kC - 1) / kC : 0;
+        const int mine = first + lane < io.n ? chunks_of(io, first + lane) : 0;
         int upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -138,7 +142,7 @@ __device__ __forceinline__ bool find_chunk(const PromptIO &io, int chunk, int *e
         if (past) {
             const int who = __ffs(past) - 1;
             *entry = first + who;
-            *at = chunk - base - __shfl_sync(0xffffffffu, upto - mine, who);
+            *at = static_cast<int>(chunk - base) - __shfl_sync(0xffffffffu, upto - mine, who);
             return true;
         }
         base += __shfl_sync(0xffffffffu, upto, 31);
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
     }
     const long long row0 = io.span.seq_start[e] + static_cast<long long>(s.item[1]) * kC;
     const int m = min(kC, io.span.length(e) - s.item[1] * kC);
-    Prepared *out = prepared(io, H, e, s.item[1], h);
+    Prepared *out = prepared(io, H, blockIdx.x, h);
 #pragma unroll
     for (int i = 0; i < kC * kD / 8 / kPrepThreads; ++i) {  // 16 threads a row
         const int t = tid / 16 + 8 * i, d = tid % 16 * 8;
@@ -405,8 +409,9 @@ struct __align__(1024) ChunkSmem {
     } rd[2];
     unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, tp_full, tp_empty, v_full, v_empty;
     unsigned long long x_full[2], k_done, r_full, u_done, u_full, y_done, x_done, drained;
+    unsigned long long before;  // chunks of the entries before this one
     uint32_t tmem;
-    int item[4];
+    int item;
 };
 
 __device__ __forceinline__ void tc_mma_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
@@ -467,14 +472,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 const int other = io.span.length(i);
                 rank += other > len || (other == len && i < tid);
             }
-            if (rank == static_cast<int>(blockIdx.x) / H) sm.item[0] = tid;
+            if (rank == static_cast<int>(blockIdx.x) / H) sm.item = tid;
         }
     } else if (tid == 0) {
-        sm.item[0] = blockIdx.x / H;
+        sm.item = blockIdx.x / H;
     }
+    if (tid == kFeedThreads) sm.before = 0;
     __syncthreads();
     launch_dependents();
-    const int e = __shfl_sync(0xffffffffu, sm.item[0], 0);
+    const int e = __shfl_sync(0xffffffffu, sm.item, 0);
     const int req = io.req_idx[e], slot = io.slot_idx[e];
     if (req < 0 || req >= pool.R || slot < 0 || slot >= pool.S) {
         wait_previous_grid();
@@ -495,6 +501,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         return;
     }
     const int chunks = (len + kC - 1) / kC;
+    {
+        unsigned long long before = 0;
+        for (int i = tid; i < e; i += kChunkThreads) before += chunks_of(io, i);
+        if (before > 0) atomicAdd(&sm.before, before);
+    }
     const long long first = io.span.seq_start[e];
     if (warp == 12) {
         if (lane == 0) {
@@ -528,7 +539,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     wait_previous_grid();  // T and P, and the states that are there already
-    const Prepared *prep = prepared(io, H, e, 0, h);
+    // (ranges that overlap may name more chunks than there is workspace for: their results are undefined, but in bounds)
+    const long long at = static_cast<long long>(sm.before);
+    const Prepared *prep = prepared(io, H, at + chunks <= prompt_chunks(io.n, io.span.total) ? at : 0, h);
     bool ok = true;
     const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, pool.waits.ns); };
     // after a wait that gave up: loads in flight land before the memory is given back (no more than one phase each is)

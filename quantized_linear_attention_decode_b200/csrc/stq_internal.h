@@ -125,7 +125,7 @@ cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t st
 // The chunked form (stq_chunk.cu), for 16-bit rows: kPreparedBytes of workspace for each chunk and head.
 constexpr int kPromptChunk = 64;
 constexpr int kPreparedBytes = 20992;
-constexpr long long prompt_chunks(int n, int total) { return static_cast<long long>(total) / kPromptChunk + n; }  // at most
+__host__ __device__ constexpr long long prompt_chunks(int n, int total) { return static_cast<long long>(total) / kPromptChunk + n; }  // at most
 cudaError_t launch_prompt_chunks(const PoolView &p, const PromptIO &io, cudaStream_t stream);
 
 // rint(fl(x / s)) for a scale s > 0 and |x / s| below 2^7 or so: a product with the reciprocal is within 2^-15 of

@@ -72,3 +72,26 @@ def test_a_state_that_is_no_number_is_in_its_column(kind, bad):
     assert not bool(y[:, 1, 5].isfinite().any())
     keep = torch.arange(128, device="cuda") != 5
     assert bool(y[:, 0].isfinite().all()) and bool(y[:, 1, keep].isfinite().all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_ranges_in_any_order(kind):
+    """A range that runs backwards is empty, so that the ones around it may lie in any order."""
+    s = _Prompts([64, 0, 128], 3, kind, seed=55)
+    s.starts = np.array([128, 192, 0, 128], np.int32)
+    s.seq_start = _cuda(s.starts)
+    s.run()
+    assert stq.stq_pool_check(s.pool, raise_on_error=False) == stq.STQ_ERR_INDEX
+    s.check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_many_ranges_in_any_order(kind):
+    """Every second range runs backwards, over more entries than the walk ranks: the blocks of rows come last to first."""
+    m, n = 70, 150
+    s = _Prompts([m if e % 2 == 0 else 0 for e in range(2 * n - 1)], 1, kind, seed=58, bits=32, fresh=[e % 3 == 0 for e in range(2 * n - 1)])
+    s.starts = np.array([(n - 1 - e // 2 + e % 2) * m for e in range(2 * n)], np.int32)
+    s.seq_start = _cuda(s.starts)
+    s.run()
+    assert stq.stq_pool_check(s.pool, raise_on_error=False) == stq.STQ_ERR_INDEX
+    s.check()
