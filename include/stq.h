@@ -524,8 +524,9 @@ stq_status stq_cache_read(stq_cache *cache, const int64_t *slot, int32_t n, floa
  *   key head h / (num_heads / num_kv_heads).
  *   page_table: device int32 [n][max_pages]; token t of sequence i is token
  *               t % 64 of page page_table[i][t / 64].  Only entries that its
- *               length reaches are read.  An entry outside the cache makes its 64
- *               tokens invisible and is reported (STQ_ERR_INDEX).
+ *               length reaches are read; max_pages is below 2^25.  An entry
+ *               outside the cache makes its 64 tokens invisible and is reported
+ *               (STQ_ERR_INDEX).
  *   seq_len:    device int32 [n], 0 <= seq_len[i] <= 64 max_pages (else the
  *               sequence is skipped, its y left as it was, and STQ_ERR_INDEX
  *               reported).  Length 0 gives y = 0.

@@ -196,6 +196,9 @@ constexpr int kUnitBytes = STQ_CACHE_BLOCK;  // a page of a head; quarters of on
 
 constexpr float kSlack = 4.0f;           // how far a score may lie above R
 
+// Pages of a table's row: a length, rounded up to a page, stays within 31 bits.
+constexpr int kMostPages = (0x7FFFFFFF - (kPage - 1)) / kPage;
+
 struct AttnArgs {
     CacheView c;
     const int32_t *table;
@@ -940,7 +943,7 @@ stq_status stq_attn_decode(stq_cache *c, const int32_t *page_table, int32_t max_
     stq_status st = stq_attn_decode_workspace(c, n, num_heads, &need);
     if (st != STQ_OK) return st;
     if (stq::dtype_bytes(dtype) == 0) return fail_status(STQ_ERR_ARG, "dtype %d", dtype);
-    if (max_pages < 0) return fail_status(STQ_ERR_ARG, "max_pages = %d", max_pages);
+    if (max_pages < 0 || max_pages > stq::kMostPages) return fail_status(STQ_ERR_ARG, "max_pages = %d", max_pages);
     if (!std::isfinite(scale)) return fail_status(STQ_ERR_ARG, "scale is not finite");
     st = stq::check_rows(q, "q", dtype, n);
     if (st != STQ_OK) return st;

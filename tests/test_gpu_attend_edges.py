@@ -1,4 +1,6 @@
 """GPU: attention of single tokens over the 4-bit cache at its edges."""
+import ctypes as C
+
 import numpy as np
 import pytest
 
@@ -49,3 +51,17 @@ def test_recycled_pages_give_the_bits_of_new_ones(lens, size):
     stq.stq_cache_append(s.cache, _cuda(stale), big, big)
     stq.stq_cache_check(s.cache, raise_on_error=False)  # (groups above binary16's range are reported, and zero)
     assert torch.equal(s.attend(), y)
+
+
+@pytest.mark.parametrize("pages", [2 ** 25, 2 ** 31 - 1, -1])
+def test_tables_too_wide_for_a_length_are_refused(pages):
+    """Lengths up to 64 max_pages are counted in 31 bits."""
+    cache = stq.stq_cache_create(1, 2)
+    q, y = (torch.zeros(1, 4, 128, device="cuda") for _ in range(2))
+    small, work = torch.zeros(64, dtype=torch.int32, device="cuda"), torch.empty(stq.stq_attn_decode_workspace(cache, 1, 4), dtype=torch.uint8, device="cuda")
+    before = stq.stq_launch_count()
+    rows = stq._Rows(q.data_ptr(), 0, 128)
+    st = stq.load().stq_attn_decode(cache.handle, small.data_ptr(), pages, small.data_ptr(), 1, 4, stq.STQ_F32, C.byref(rows), 0.1,
+                                    y.data_ptr(), work.data_ptr(), work.numel(), 0)
+    assert st == stq.STQ_ERR_ARG and "max_pages" in stq.stq_last_error()
+    assert stq.stq_launch_count() == before
