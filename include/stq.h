@@ -421,7 +421,7 @@ typedef struct {
  *   workspace: device scratch of at least stq_prompt_workspace bytes, 16-byte
  *              aligned, owned by the caller; its content need not be kept between
  *              calls.  Calls that may overlap on the GPU need one each, and a
- *              state each.
+ *              state each.  fp32 rows need none (NULL and 0 will do).
  * A NaN in a token's q makes its y of that head NaN; one in its k, v, beta or alpha
  * (or in the starting state) the state and y that depend on it, from that token on,
  * and with 16-bit rows y of up to 63 tokens before it may be NaN too.  A state that

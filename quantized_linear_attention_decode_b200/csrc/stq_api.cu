@@ -637,7 +637,7 @@ stq_status stq_prompt_workspace(const stq_pool *p, int32_t n, int32_t total, siz
 {
     if (p == nullptr || bytes == nullptr) return fail(STQ_ERR_ARG, "NULL argument");
     if (n < 0 || total < 0) return fail(STQ_ERR_ARG, "n = %d, total = %d", n, total);
-    // whatever the type of the rows turns out to be
+    // for 16-bit rows; fp32 rows take none
     *bytes = std::max<size_t>(256, (size_t)stq::prompt_chunks(n, total) * p->H * stq::kPreparedBytes);
     return STQ_OK;
 }
@@ -653,10 +653,11 @@ stq_status stq_prompt_step(stq_pool *p, const int32_t *req_idx, const int32_t *s
     size_t need = 0;
     st = stq_prompt_workspace(p, n, total, &need);
     if (st != STQ_OK) return st;
+    if (dtype == STQ_F32) need = 0;
     if (p->kind != STQ_GDN) return fail(STQ_ERR_UNSUPPORTED, "prompts need a GDN pool (one decay a head and token)");
     if (stq::dtype_bytes(dtype) == 0) return fail(STQ_ERR_ARG, "dtype %d", dtype);
     if (q == nullptr || k == nullptr || v == nullptr) return fail(STQ_ERR_ARG, "q, k or v is NULL");
-    if (n > 0 && (seq_start == nullptr || state == nullptr || workspace == nullptr))
+    if (n > 0 && (seq_start == nullptr || state == nullptr || (need > 0 && workspace == nullptr)))
         return fail(STQ_ERR_ARG, "a seq_start/state/workspace pointer is NULL");
     if (n > 0 && total > 0 && (!q->data || !k->data || !v->data || !beta || !alpha || !y))
         return fail(STQ_ERR_ARG, "a q/k/v/beta/alpha/y pointer is NULL");

@@ -496,7 +496,7 @@ def _scratch(workspace, nbytes, index, stream):
 
 
 def stq_prompt_workspace(pool: Pool, n: int, total: int) -> int:
-    """Bytes of scratch that stq_prompt_step needs for n prompts in `total` token rows."""
+    """Bytes of scratch that stq_prompt_step needs for n prompts in `total` token rows of 16 bits (of fp32: none)."""
     a = C.c_size_t()
     _check(load().stq_prompt_workspace(pool.handle, int(n), int(total), C.byref(a)))
     return a.value
@@ -514,7 +514,10 @@ def stq_prompt_step(pool: Pool, req_idx, slot_idx, seq_start, q, k, v, beta, alp
     n, total, dev, dt, i32, f = req_idx.numel(), q.shape[0], pool.device.index, q.dtype, torch.int32, torch.float32
     kind, shape = _dtype(q, "q"), (total, pool.H, 128)
     qr, kr, vr = (_rows(t, dt, dev, shape, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
-    work, nbytes, keep = _scratch(workspace, 0 if workspace is not None else stq_prompt_workspace(pool, n, total), dev, stream)
+    if workspace is None and kind == STQ_F32:
+        work, nbytes, keep = None, 0, None
+    else:
+        work, nbytes, keep = _scratch(workspace, 0 if workspace is not None else stq_prompt_workspace(pool, n, total), dev, stream)
     _check(load().stq_prompt_step(
         pool.handle, _flat(req_idx, i32, dev, (n,), "req_idx"), _flat(slot_idx, i32, dev, (n,), "slot_idx"), n,
         _flat(seq_start, i32, dev, (n + 1,), "seq_start"), total,

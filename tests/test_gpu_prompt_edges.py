@@ -95,3 +95,18 @@ def test_many_ranges_in_any_order(kind):
     s.run()
     assert stq.stq_pool_check(s.pool, raise_on_error=False) == stq.STQ_ERR_INDEX
     s.check()
+
+
+def test_fp32_rows_need_no_workspace():
+    s = _Prompts([2000, 96], 8, "fp32", seed=57, state=False)
+    y, state = (t.clone() for t in s.run())
+    torch.cuda.synchronize()
+    y2, state2 = torch.zeros_like(y), torch.zeros_like(state)
+    args = (s.pool, s.req, s.slot, s.seq_start, s.q, s.k, s.v, s.beta, s.alpha, y2, state2)
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    stq.stq_prompt_step(*args, fresh=s.fresh)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 16
+    assert torch.equal(y2, y) and torch.equal(state2, state)
+    stq.stq_prompt_step(*args, fresh=s.fresh, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(y2, y) and torch.equal(state2, state)
