@@ -159,6 +159,9 @@ stq_status stq_pool_destroy(stq_pool *pool);
  * (request, slot)). */
 stq_status stq_pool_bytes(const stq_pool *pool, size_t *packed_bytes, size_t *per_slot_bytes);
 
+/* The device that holds the pool: the current one when it was created. */
+stq_status stq_pool_device(const stq_pool *pool, int32_t *device);
+
 /* The same figures for a description, computed on the host without
  * allocating anything (no device needed). */
 stq_status stq_desc_bytes(const stq_pool_desc *desc, size_t *packed_bytes, size_t *per_slot_bytes);

@@ -11,7 +11,7 @@ from .stq import (  # noqa: F401
     stq_allocate_bits, stq_lifetime_weight, stq_decode_step_static, stq_decode_step_host,
     stq_decode_step_host_block, stq_host_block_layout,
     stq_export_slot, stq_import_slot, stq_last_error, stq_launch_count, stq_page_layout,
-    stq_pool_bytes, stq_pool_check, stq_pool_create, stq_pool_destroy, stq_quantize_state,
+    stq_pool_bytes, stq_pool_check, stq_pool_create, stq_pool_destroy, stq_pool_device, stq_quantize_state,
     stq_status_str,
     STQ_BF16, STQ_CACHE_PAGE, STQ_F16, STQ_F32, Cache, stq_attn_decode, stq_attn_decode_workspace, stq_cache_append,
     stq_cache_bytes, stq_cache_check, stq_cache_create, stq_cache_destroy, stq_cache_read,

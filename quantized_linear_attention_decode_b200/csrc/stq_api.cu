@@ -474,6 +474,13 @@ stq_status stq_pool_bytes(const stq_pool *p, size_t *packed_bytes, size_t *per_s
     return STQ_OK;
 }
 
+stq_status stq_pool_device(const stq_pool *p, int32_t *device)
+{
+    if (p == nullptr || device == nullptr) return fail(STQ_ERR_ARG, "NULL argument");
+    *device = p->device;
+    return STQ_OK;
+}
+
 stq_status stq_page_layout(const stq_pool *p, int32_t head, size_t *offset_in_slot,
                            size_t *page_bytes)
 {

@@ -35,7 +35,7 @@ EXPORTS = ("stq_pool_create", "stq_pool_destroy", "stq_pool_bytes", "stq_desc_by
            "stq_status_str", "stq_last_error",
            "stq_cache_create", "stq_cache_destroy", "stq_cache_bytes", "stq_cache_append", "stq_cache_read",
            "stq_attn_decode_workspace", "stq_attn_decode", "stq_cache_check",
-           "stq_prompt_workspace", "stq_prompt_step", "stq_attn_prompt")
+           "stq_prompt_workspace", "stq_prompt_step", "stq_attn_prompt", "stq_pool_device")
 
 
 class StqError(RuntimeError):
@@ -90,6 +90,7 @@ def load():
         "stq_export_slot": [P, I32, I32, P, SZ],
         "stq_import_slot": [P, I32, I32, P, SZ],
         "stq_pool_check": [P, P],
+        "stq_pool_device": [P, P],
         "stq_prompt_workspace": [P, I32, I32, P],
         "stq_prompt_step": [P, P, P, I32, P, I32, P, I32, P, P, P, P, P, P, P, P, SZ, P],
         "stq_attn_prompt": [P, P, I32, I32, I32, I32, I32, I32, P, P, P, C.c_float, P, P, P],
@@ -159,9 +160,8 @@ class Pool:
     """Owner of one stq_pool handle (destroyed with the object)."""
 
     def __init__(self, handle, kind, R, S, H, unit_bits, flags=0):
-        import torch
         self.handle = handle
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device_index = stq_pool_device(self)
         self.kind, self.R, self.S, self.H = kind, R, S, H
         self.unit_bits = np.asarray(unit_bits, np.uint8).copy()
         self.flags = int(flags)
@@ -177,6 +177,11 @@ class Pool:
                 _lib.stq_pool_destroy(h)
             except Exception:  # noqa: BLE001  (interpreter shutdown)
                 pass
+
+    @property
+    def device(self):
+        import torch
+        return torch.device("cuda", self.device_index)
 
     @property
     def row_bits(self) -> np.ndarray:
@@ -207,6 +212,13 @@ def stq_pool_bytes(pool: Pool):
     a, b = C.c_size_t(), C.c_size_t()
     _check(load().stq_pool_bytes(pool.handle, C.byref(a), C.byref(b)))
     return a.value, b.value
+
+
+def stq_pool_device(pool: Pool) -> int:
+    """The number of the CUDA device that holds the pool."""
+    a = C.c_int32()
+    _check(load().stq_pool_device(pool.handle, C.byref(a)))
+    return a.value
 
 
 def stq_desc_bytes(kind, num_requests, num_slots, num_heads, unit_bits, row_factor=None,
@@ -511,7 +523,7 @@ def stq_prompt_step(pool: Pool, req_idx, slot_idx, seq_start, q, k, v, beta, alp
     import torch
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [total, H, 128] tensor")
-    n, total, dev, dt, i32, f = req_idx.numel(), q.shape[0], pool.device.index, q.dtype, torch.int32, torch.float32
+    n, total, dev, dt, i32, f = req_idx.numel(), q.shape[0], pool.device_index, q.dtype, torch.int32, torch.float32
     kind, shape = _dtype(q, "q"), (total, pool.H, 128)
     qr, kr, vr = (_rows(t, dt, dev, shape, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
     if workspace is None and kind == STQ_F32:

@@ -98,3 +98,8 @@ def test_bindings_refuse_host_tensors():
         stq.stq_attn_prompt(s, s, x, x, x, x)
     with pytest.raises(ValueError):
         stq.stq_attn_prompt(s, s, x[0], x, x, x)
+
+
+def test_pool_device_refuses():
+    a = C.c_int32()
+    assert stq.STATUS[stq.load().stq_pool_device(None, C.byref(a))] == "STQ_ERR_ARG"
