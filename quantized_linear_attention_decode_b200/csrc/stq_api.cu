@@ -187,7 +187,7 @@ stq::PoolView view(stq_pool *p)
     v.n_pivot_heads = p->n_pivot_heads;
     v.t = p->t;
     v.err = p->d_err;
-    v.waits = stq::waits();
+    static_cast<stq::Waits &>(v) = stq::waits();
     return v;
 }
 

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_tile = kRows / a.pack;  // tokens of a query tile
     bool ok = true;
 
-    const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, a.waits.ns); };
+    const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, a.waits.wait_ns); };
     // Item n of this CTA, a value a lane; false: no more.  The whole warp calls these.
     int entry = 0;
     const auto take = [&](int n) {

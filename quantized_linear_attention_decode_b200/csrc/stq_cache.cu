@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel
         begin_segment(a, sg, w.seq, h0, nh);
         for (int u = u0; u < u1; ++u) {
             const int k = taken % kStagesW;
-            if (!__all_sync(0xffffffffu, barrier_wait(bar0 + 8 * k, taken / kStagesW & 1, a.waits.ns))) {
+            if (!__all_sync(0xffffffffu, barrier_wait(bar0 + 8 * k, taken / kStagesW & 1, a.waits.wait_ns))) {
                 if (lane == 0) atomicOr(a.c.err, kErrTimeout);
                 dead = true;
                 break;
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAttnCtas<NT>) attn_decode_kernel
     }
     // after a wait that gave up, let the copies in flight land (bounded) before the memory is given back
     if (dead)
-        for (; taken < issued; ++taken) barrier_wait(bar0 + 8 * (taken % kStagesW), taken / kStagesW & 1, a.waits.ns);
+        for (; taken < issued; ++taken) barrier_wait(bar0 + 8 * (taken % kStagesW), taken / kStagesW & 1, a.waits.wait_ns);
 }
 
 // Joins the partial sums of one (sequence, query head) in the order of the warps

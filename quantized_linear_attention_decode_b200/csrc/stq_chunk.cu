@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const long long at = static_cast<long long>(sm.before);
     const Prepared *prep = prepared(io, H, at + chunks <= prompt_chunks(io.n, io.span.total) ? at : 0, h);
     bool ok = true;
-    const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, pool.waits.ns); };
+    const auto wait = [&](unsigned long long &b, uint32_t parity) { return barrier_wait(smem_addr(&b), parity, pool.wait_ns); };
     // after a wait that gave up: loads in flight land before the memory is given back (no more than one phase each is)
     const auto drain = [&] {
         if (tid == kGroupThreads || tid == kGroupThreads + kFeedThreads + 32)
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         const int ft = tid - kGroupThreads, fw = warp - 8;
         const auto fetch = [&](int c) {  // as they are, by one thread
             const uint32_t bar = smem_addr(&sm.kq_raw);
-            barrier_expect(bar, 4 * kC * 128 + (c == 0 && blockIdx.x == 0 ? pool.waits.stall_tx : 0));
+            barrier_expect(bar, 4 * kC * 128 + (c == 0 && blockIdx.x == 0 ? pool.stall_tx : 0));
             for (int half = 0; half < 2; ++half) {
                 tma_load3(smem_addr(sm.raw_k[half]), &k_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);
                 tma_load3(smem_addr(sm.raw_q[half]), &q_map, bar, 64 * half, h, static_cast<int>(first) + c * kC);

@@ -994,13 +994,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(PoolView p, DecodeI
     if (tid == 0)
         for (int a = 0; a < 3; ++a)
             if (first + a * G < tiles)
-                issue<KIND>(sm, a, p, resolve(p, raw_from_smem(sm, a)), first == 0 && a == 0 ? p.waits.stall_tx : 0u);
+                issue<KIND>(sm, a, p, resolve(p, raw_from_smem(sm, a)), first == 0 && a == 0 ? p.stall_tx : 0u);
     cp_async_wait<0>();
     __syncthreads();  // the first vectors and the stages' validity are visible
     bool timed_out = false;
     if (tid >= kD) {
         // warp-uniform outcome: row_setup's shuffles need every lane
-        if (__all_sync(0xffffffffu, mbar_wait_bounded(&sm.full[0], 0, p.waits.ns))) row_setup<KIND, SB, MODE, FIT>(sm, sm.st[0], sm.rc[0], 0);
+        if (__all_sync(0xffffffffu, mbar_wait_bounded(&sm.full[0], 0, p.wait_ns))) row_setup<KIND, SB, MODE, FIT>(sm, sm.st[0], sm.rc[0], 0);
         else timed_out = true;
     }
     timed_out = __syncthreads_or(timed_out) != 0;
@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(PoolView p, DecodeI
         } else {
             if (tile + G < tiles) {
                 const int sn = (i + 1) % kStages;
-                if (__all_sync(0xffffffffu, mbar_wait_bounded(&sm.full[sn], ((i + 1) / kStages) & 1, p.waits.ns)))
+                if (__all_sync(0xffffffffu, mbar_wait_bounded(&sm.full[sn], ((i + 1) / kStages) & 1, p.wait_ns)))
                     row_setup<KIND, SB, MODE, FIT>(sm, sm.st[sn], sm.rc[(i + 1) & 1], sn);
                 else if ((tid & 31) == 0)
                     sm.stop = 1;
@@ -1100,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(PoolView p, DecodeI
             atomicOr(p.err, kErrTimeout);
             for (int k = i; k < i + 3; ++k) {
                 const int t = first + k * G;
-                if (t < tiles) mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, p.waits.ns);
+                if (t < tiles) mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, p.wait_ns);
             }
         }
         if (sm.flags) atomicOr(p.err, sm.flags);

@@ -25,15 +25,7 @@ inline bool fault(const char *which)
 }
 
 // STQ_FAULT=timeout: a wait that nothing completes, given a short limit.
-inline Waits waits()
-{
-    Waits w;
-    if (fault("timeout")) {
-        w.ns = 2000000ull;
-        w.stall_tx = 16;
-    }
-    return w;
-}
+inline Waits waits() { return fault("timeout") ? Waits{2000000ull, 16u} : Waits{1000000000ull, 0u}; }
 
 // An NVTX range over a launching call (a no-op unless a profiler is attached),
 // so that profiles attribute device work to the entry point that queued it.

@@ -48,11 +48,11 @@ struct Tables {
 
 // How long device-side waits last, and a test hook: bytes that the first barrier of a launch expects beyond its copies.
 struct Waits {
-    unsigned long long ns = 1000000000ull;  // limit of every bounded wait
-    uint32_t stall_tx = 0;
+    unsigned long long wait_ns;  // limit of every bounded wait
+    uint32_t stall_tx;
 };
 
-struct PoolView {
+struct PoolView : Waits {
     uint8_t *pages;      // [R][S][slot_bytes]
     size_t slot_bytes;
     int R, S, H;
@@ -66,7 +66,6 @@ struct PoolView {
     int n_pivot_heads;   // GDN: heads held in FP16 (their own kernel), listed in t.pivot_head
     Tables t;
     uint32_t *err;
-    Waits waits;
 };
 
 struct DecodeIO {
