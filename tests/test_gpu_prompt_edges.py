@@ -110,3 +110,25 @@ def test_fp32_rows_need_no_workspace():
     assert torch.equal(y2, y) and torch.equal(state2, state)
     stq.stq_prompt_step(*args, fresh=s.fresh, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert torch.equal(y2, y) and torch.equal(state2, state)
+
+
+@pytest.mark.parametrize("flags", [stq.STQ_SCALE_F16, stq.STQ_FIT_COLUMNS, stq.STQ_FIT_COLUMNS | stq.STQ_SCALE_F16])
+@pytest.mark.parametrize("kind, lens", [("bf16", [5, 0, 70, 130, 0]), ("fp32", [5, 0, 70, 1, 0]), ("fp16", [3, 0, 1, 9, 0])])
+def test_pools_of_other_formats(flags, kind, lens):
+    """binary16 scales and fitted columns, 16-bit pivot heads among them: pages are read before and quantized after as the
+    calls of their own do it, byte for byte."""
+    class P(_Prompts):
+        def new_pool(self, slots=2):
+            return stq.stq_pool_create(stq.STQ_GDN, self.n, slots, self.H, self.bits, flags=flags)
+
+    s = P(lens, 4, kind, seed=56, bits=np.array([6, 16, 4, 8], np.uint8), fresh=[0, 1, 0, 1, 0])
+    before = s.pages(s.pool, 4)
+    y, state = s.run()
+    stq.stq_pool_check(s.pool)
+    s.check()
+    twin = s.new_pool()
+    state[4] = 0
+    stq.stq_quantize_state(twin, s.req, s.slot, state)
+    for e in range(4):
+        assert np.array_equal(s.pages(s.pool, e), s.pages(twin, e)), e
+    assert np.array_equal(s.pages(s.pool, 4), before)
