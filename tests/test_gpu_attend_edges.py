@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from quantized_linear_attention_decode_b200 import stq
-from test_gpu_cache import _Sequences, _cuda
+from test_gpu_cache import _Sequences, _cuda, _quantized
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -51,6 +51,48 @@ def test_recycled_pages_give_the_bits_of_new_ones(lens, size):
     stq.stq_cache_append(s.cache, _cuda(stale), big, big)
     stq.stq_cache_check(s.cache, raise_on_error=False)  # (groups above binary16's range are reported, and zero)
     assert torch.equal(s.attend(), y)
+
+
+class _Fp32(_Sequences):
+    def check_fp32(self, y, scale=128 ** -0.5):
+        """fp32 rows: q, the weights and their products with the scales are two binary16 terms each (2^-22 of them is left);
+        a score's sum of 128 products is off by less than 2^-19 of their sizes, a weight by twice a score's error; exp2, the
+        sums and the join by 2^-18 together; terms that are subnormal by half of 2^-24, as _Sequences.check has it."""
+        got = y.cpu().numpy().astype(np.float64)
+        k, v = (_quantized(x.cpu().numpy()).astype(np.float64) for x in (self.k, self.v))
+        q = self.q.cpu().numpy().astype(np.float64)
+        g, at = self.heads // self.kv_heads, 0
+        for i, m in enumerate(self.lens):
+            for h in range(self.heads):
+                kk, vv = k[at:at + m, h // g], v[at:at + m, h // g]
+                x = kk @ q[i, h] * scale
+                p = np.exp(x - x.max())
+                p /= p.sum()
+                ref = p @ vv
+                delta = (np.abs(kk) @ np.abs(q[i, h])).max() * abs(scale) * (2.0 ** -19 + 2.0 ** -21)
+                s_max = np.abs(vv).max() / 7 * 1.01
+                small = 2.0 ** -36 * p.max() * max(1.0, 2 * s_max) * (1 + s_max) * 7 * m
+                tol = small + (2.0 ** -18 + 2 * delta + 2.0 ** -20) * (p @ np.abs(vv)) + 2.0 ** -24 * np.abs(ref)
+                bad = ~(np.abs(got[i, h] - ref) <= tol)
+                assert not bad.any(), (i, h, m, np.abs(got[i, h] - ref)[bad][:4], tol[bad][:4])
+            at += m
+
+
+@pytest.mark.parametrize("heads, kv_heads", [(1, 1), (8, 2), (9, 1), (32, 2), (40, 2)])
+@pytest.mark.parametrize("spread", [0.3, 1.0, 3.0])
+def test_fp32_rows_keep_fp32(heads, kv_heads, spread):
+    s = _Fp32([1, 63, 64, 65, 200, 1000], heads, kv_heads, "fp32", seed=34, spread=spread)
+    s.append()
+    y = s.attend()
+    s.check_fp32(y)
+    assert torch.equal(y, s.attend())
+
+
+@pytest.mark.parametrize("lens", [[30000], [70] * 150])
+def test_fp32_rows_over_many_shares(lens):
+    s = _Fp32(lens, 8, 2, "fp32", seed=35)
+    s.append()
+    s.check_fp32(s.attend())
 
 
 @pytest.mark.parametrize("pages", [2 ** 25, 2 ** 31 - 1, -1])
