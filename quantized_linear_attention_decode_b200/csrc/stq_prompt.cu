@@ -361,12 +361,15 @@ cudaError_t launch_tokens(const PoolView &p, const PromptIO &io, cudaStream_t st
 
 cudaError_t launch_prompt(const PoolView &p, const PromptIO &io, cudaStream_t stream)
 {
-    // 16-bit rows (that a tensor map can describe) go in chunks of 64 tokens; fewer tokens than that, whatever prompts they
-    // are shared out into, are as fast or faster without (one prompt of 37 tokens on 4 heads 17 against 25 us, of 64 21 us
-    // both, of 80 25 against 23; 4 prompts of 15 tokens on 32 heads 25 against 34 us)
+    // 16-bit rows (that a tensor map can describe) go in chunks of 64 tokens, which take as long for one token as for 64.  Four at a
+    // time is faster up to 64 tokens where entries are few (one entry on 32 heads: 10 against 23 us for one token, 23 both for
+    // 64, 31 against 27 for 96), up to 24 where they are many (64 on 32 heads: 166 against 269 us for one token each, 278 against
+    // 275 for 24, 508 against 284 for 64).  The host knows only their sum, of which one entry may have nearly all (60 of one
+    // token and 4 of 1000: 605 against 359 us): so below 64 and two for each further entry, where even then the longest is
+    // short.
     const int total = io.span.total;
-    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= kPromptChunk && rows_mappable(io.q, p.H, total) && rows_mappable(io.k, p.H, total) &&
-        rows_mappable(io.v, p.H, total))
+    if (io.dtype != STQ_F32 && p.H <= 65535 && total >= kPromptChunk + 2ll * (io.n - 1) && rows_mappable(io.q, p.H, total) &&
+        rows_mappable(io.k, p.H, total) && rows_mappable(io.v, p.H, total))
         return launch_prompt_chunks(p, io, stream);
     const long long units = static_cast<long long>(io.n) * p.H;
     // more lanes a column shorten a block's latency and cost each warp more loads and exchanges a column: 16 against

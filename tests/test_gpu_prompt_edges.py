@@ -132,3 +132,16 @@ def test_pools_of_other_formats(flags, kind, lens):
     for e in range(4):
         assert np.array_equal(s.pages(s.pool, e), s.pages(twin, e)), e
     assert np.array_equal(s.pages(s.pool, 4), before)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens, launches", [([1] * 100, 3), ([2] * 70 + [0] * 9, 3), ([1] * 100 + [300], 4), ([64], 4), ([63], 3)])
+def test_entries_of_few_tokens_each(kind, lens, launches):
+    """A step of single tokens takes no chunks however many entries it has (unpack, advance, quantize: three launches; a
+    fourth prepares chunks), and with a prompt beside them all are as right."""
+    s = _Prompts(lens, 2, kind, seed=59, fresh=[e % 2 for e in range(len(lens))])
+    before = stq.stq_launch_count()
+    s.run()
+    assert stq.stq_launch_count() - before == launches
+    stq.stq_pool_check(s.pool)
+    s.check()
