@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (warp == 8) {
             // ------------------------------------------------ loads
-            int queries = 0, tile = 0;  // loads of queries and key tiles so far
+            int queries = 0, tile = 0, values = 0;  // loads of queries, key tiles and their values so far
             for (int n = 0; take(n); ++n) {
                 const int tiles[2] = {tiles_of(keys_of(0)), tiles_of(keys_of(1))}, all = max(tiles[0], tiles[1]);
                 const int q_row = value(0) + value(4), k_row = value(2), block = value(5), kv_head = block / (a.group / a.pack);
@@ -285,11 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         barrier_expect(kf, kTileBytes + (tile == 0 && blockIdx.x == 0 ? a.waits.stall_tx : 0));
                         for (int half = 0; half < 2; ++half)
                             tma_load3(smem_addr(sm.k[s]) + half * kHalfTile, &k_map, kf, 64 * half, kv_head, k_row + j * kRows);
-                        ok = tile < kStages || wait(sm.v_empty[s], parity);
+                        ++tile;
+                        ok = values < kStages || wait(sm.v_empty[s], parity);
+                        if (!ok) break;
                         barrier_expect(vf, kTileBytes);
                         for (int half = 0; half < 2; ++half)
                             tma_load3(smem_addr(sm.v[s]) + half * kHalfTile, &v_map, vf, 64 * half, kv_head, k_row + j * kRows);
-                        ++tile;
+                        ++values;
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
@@ -299,10 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok && lane == 0) {  // the loads in flight land before the memory is given back
                 if (queries > 0) wait(sm.q_full, (queries - 1) & 1);
-                for (int j = max(0, tile - kStages); j < tile; ++j) {
-                    wait(sm.k_full[j % kStages], j / kStages & 1);
-                    wait(sm.v_full[j % kStages], j / kStages & 1);
-                }
+                for (int j = max(0, tile - kStages); j < tile; ++j) wait(sm.k_full[j % kStages], j / kStages & 1);
+                for (int j = max(0, values - kStages); j < values; ++j) wait(sm.v_full[j % kStages], j / kStages & 1);
             }
             __syncwarp();
         }
