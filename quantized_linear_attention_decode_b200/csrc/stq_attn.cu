@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) barrier_arrive(smem_addr(&sm.wanted));
                 taken(n);
             }
-            if (!ok && lane == 0) {  // the loads in flight land before the memory is given back
+            if (lane == 0) {  // the loads land before the memory is given back, whatever became of those who wanted them
                 if (queries > 0) wait(sm.q_full, (queries - 1) & 1);
                 for (int j = max(0, tile - kStages); j < tile; ++j) wait(sm.k_full[j % kStages], j / kStages & 1);
                 for (int j = max(0, values - kStages); j < values; ++j) wait(sm.v_full[j % kStages], j / kStages & 1);

@@ -674,6 +674,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     if (ok) fetch_v(c + 1);
                 }
             }
+            if (ok && ft == 0) wait(sm.v_full, (chunks - 1) & 1);  // lands, whatever became of those who wanted it
         } else if (warp == 12) {
             // ------------------------------------------------ products
             constexpr uint32_t n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
