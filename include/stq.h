@@ -539,9 +539,9 @@ stq_status stq_cache_read(stq_cache *cache, const int64_t *slot, int32_t n, floa
  *               16-byte aligned, owned by the caller; its content need not be
  *               kept between calls.  Calls that may overlap on the GPU (streams,
  *               captured graphs) need one each.
- * Scores and sums are fp32.  With 16-bit rows a weight and its product with a value's
- * scale are rounded to binary16 (2^-11 of each); with fp32 rows 2^-22 of them, and of
- * q, stays behind.
+ * Scores and sums are fp32.  With bf16 rows a weight and its product with a value's
+ * scale are rounded to binary16 (2^-11 of each); with fp16 and fp32 rows 2^-22 of
+ * them, and of an fp32 q, stays behind.
  * The same call gives the same bits: partial sums are joined in a fixed order.
  * A head whose q is not finite (or not below 2^100) has an unspecified y.
  */

@@ -184,16 +184,17 @@ __global__ void __launch_bounds__(256) read_kernel(CacheView c, const long long 
 //                  a token in place of 32 conversions.
 //   O^T += V^T P^T 16 dims x 8 heads a tile; a value's scale goes into P.  P is
 //                  rounded to binary16, and so is its product with the scale: 2^-11 of a
-//                  weight each, below the output's own rounding in bf16 and like it in fp16.
+//                  weight each, below the output's own rounding in bf16.
 // P is 2^11 exp2(x - R) with R at least the running maximum, less 4, of x + max(0, log2 of the
 // unit's largest value scale), so that P times a scale stays below 2^15 while small
 // weights keep their bits: what falls below binary16's subnormals is 2^-36 of the
 // largest weight.  Sums are fp32.
 //
-// fp32 rows (WIDE) keep their bits: q, P and P's product with a scale are two binary16 values
-// each, the second what rounding to the first left, and both meet the codes: 2^-22 of them
-// stays behind, for twice the products (64 sequences to 8192 tokens, 32/8 heads: 93 us
-// against 77 for 16-bit rows, whose q is exact in one value).
+// For fp16 and fp32 rows P, and P's product with a scale, are two binary16 values each
+// (TERMS_P), the second what rounding to the first left, and both meet the codes: 2^-22 of a
+// weight stays behind, for twice the products.  So is q for fp32 rows (TERMS_Q; of 16 bits it
+// is exact in one).  64 sequences to 8192 tokens, 32/8 heads: 77 us in bf16, 86 in fp16 (with
+// one value 75, and 1.6 times the error of the output's own rounding), 93 in fp32.
 
 constexpr int kWarps = 4;   // of a CTA; they share nothing but its memory
 constexpr int kStagesW = 2;  // units in a warp's ring
@@ -361,10 +362,9 @@ __device__ __forceinline__ uint32_t rest_of(float2 x, __half2 h)
 __device__ __forceinline__ float2 floats_of(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
 // The running state of one segment: lane (g, t) has columns 2t, 2t + 1 of each block of eight heads.
-template <int NT, bool WIDE>
+template <int NT, int TERMS_Q>
 struct Segment {
-    static constexpr int kTerms = WIDE ? 2 : 1;
-    uint32_t qf[kTerms][NT][4][4];  // q as B fragments
+    uint32_t qf[TERMS_Q][NT][4][4];  // q as B fragments
     float fac[NT][2];       // from products of codes to scores in units of log 2
     float o[8][NT][4], top[NT][2], weight[NT][2];
 };
@@ -372,8 +372,8 @@ struct Segment {
 // q: step (group gi, j) takes dims 32 gi + 8 t + j and + 4 + j of head g, scaled by a power of two
 // so that every row lies high in binary16's range (the largest value in [2^13, 2^14): a 16-bit q is
 // exact down to 2^-20 of it), and by 1 / 16 where the codes come as 16 u.
-template <int NT, bool WIDE>
-__device__ __forceinline__ void begin_segment(const AttnArgs &a, Segment<NT, WIDE> &sg, int seq, int h0, int nh)
+template <int NT, int TERMS_Q>
+__device__ __forceinline__ void begin_segment(const AttnArgs &a, Segment<NT, TERMS_Q> &sg, int seq, int h0, int nh)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -405,7 +405,7 @@ __device__ __forceinline__ void begin_segment(const AttnArgs &a, Segment<NT, WID
                 const float2 f = make_float2(x[gi][j] * fold, x[gi][4 + j] * fold);
                 const __half2 v = __floats2half2_rn(f.x, f.y);
                 sg.qf[0][nt][gi][j] = *reinterpret_cast<const uint32_t *>(&v);
-                if (WIDE) sg.qf[Segment<NT, WIDE>::kTerms - 1][nt][gi][j] = rest_of(f, v);
+                if (TERMS_Q == 2) sg.qf[TERMS_Q - 1][nt][gi][j] = rest_of(f, v);
             }
         }
         sg.fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
@@ -443,10 +443,10 @@ __device__ __forceinline__ void pairs_of(uint32_t w, uint32_t (&p)[4])
 
 // MT tiles of 16 tokens in shared memory, from tile m0 on; `valid` of the tokens there are the
 // sequence's, at least one of them in these tiles.
-template <int NT, bool WIDE, int MT>
-__device__ __forceinline__ void take_unit(Segment<NT, WIDE> &sg, const uint8_t *b, int valid, int m0)
+template <int NT, int TERMS_Q, int TERMS_P, int MT>
+__device__ __forceinline__ void take_unit(Segment<NT, TERMS_Q> &sg, const uint8_t *b, int valid, int m0)
 {
-    constexpr int kLast = Segment<NT, WIDE>::kTerms - 1;
+    constexpr int kLast = TERMS_Q - 1, kLastP = TERMS_P - 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float x[MT][NT][4];  // scores in units of fac
 #pragma unroll
@@ -562,7 +562,7 @@ __device__ __forceinline__ void take_unit(Segment<NT, WIDE> &sg, const uint8_t *
         const uint4 ub = *reinterpret_cast<const uint4 *>(bh + kValueScales + 16 * (pr + 4));
         const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
         const uint32_t fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w};
-        __half2 b0[kLast + 1][NT], b1[kLast + 1][NT];
+        __half2 b0[TERMS_P][NT], b1[TERMS_P][NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float e[4];
@@ -573,9 +573,9 @@ __device__ __forceinline__ void take_unit(Segment<NT, WIDE> &sg, const uint8_t *
             const __half2 c0 = __floats2half2_rn(e[0], e[1]), c1 = __floats2half2_rn(e[2], e[3]);
             b0[0][nt] = halves(transpose8(*reinterpret_cast<const uint32_t *>(&c0)));
             b1[0][nt] = halves(transpose8(*reinterpret_cast<const uint32_t *>(&c1)));
-            if (WIDE) {
-                b0[kLast][nt] = halves(transpose8(rest_of(make_float2(e[0], e[1]), c0)));
-                b1[kLast][nt] = halves(transpose8(rest_of(make_float2(e[2], e[3]), c1)));
+            if (TERMS_P == 2) {
+                b0[kLastP][nt] = halves(transpose8(rest_of(make_float2(e[0], e[1]), c0)));
+                b1[kLastP][nt] = halves(transpose8(rest_of(make_float2(e[2], e[3]), c1)));
             }
         }
 #pragma unroll
@@ -587,9 +587,9 @@ __device__ __forceinline__ void take_unit(Segment<NT, WIDE> &sg, const uint8_t *
             for (int nt = 0; nt < NT; ++nt) {
                 const __half2 s0 = halves(fa[gi]), s1 = halves(fb[gi]);
                 const __half2 e0 = __hmul2(b0[0][nt], s0), e1 = __hmul2(b1[0][nt], s1);
-                if (WIDE) {  // what the product's rounding left (a fused multiply-add has it), and the second value's product
-                    const __half2 r0 = __hfma2(b0[kLast][nt], s0, __hfma2(b0[0][nt], s0, __hneg2(e0)));
-                    const __half2 r1 = __hfma2(b1[kLast][nt], s1, __hfma2(b1[0][nt], s1, __hneg2(e1)));
+                if (TERMS_P == 2) {  // what the product's rounding left (a fused multiply-add has it), and the second value's product
+                    const __half2 r0 = __hfma2(b0[kLastP][nt], s0, __hfma2(b0[0][nt], s0, __hneg2(e0)));
+                    const __half2 r1 = __hfma2(b1[kLastP][nt], s1, __hfma2(b1[0][nt], s1, __hneg2(e1)));
                     const uint32_t v0 = *reinterpret_cast<const uint32_t *>(&r0), v1 = *reinterpret_cast<const uint32_t *>(&r1);
                     mma_f16(sg.o[2 * gi][nt], pa[0], pa[1], pb[0], pb[1], v0, v1);
                     mma_f16(sg.o[2 * gi + 1][nt], pa[2], pa[3], pb[2], pb[3], v0, v1);
@@ -621,8 +621,8 @@ __device__ __forceinline__ void store4(void *y, int64_t at, int dtype, const flo
 }
 
 // The segment's result: y itself where the warp had all of it (part == nullptr), else a partial.
-template <int NT, bool WIDE>
-__device__ __forceinline__ void end_segment(const AttnArgs &a, Segment<NT, WIDE> &sg, int seq, int h0, int nh, float *part)
+template <int NT, int TERMS_Q>
+__device__ __forceinline__ void end_segment(const AttnArgs &a, Segment<NT, TERMS_Q> &sg, int seq, int h0, int nh, float *part)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -650,8 +650,8 @@ __device__ __forceinline__ void end_segment(const AttnArgs &a, Segment<NT, WIDE>
 
 constexpr int attn_ctas(int nt, bool wide) { return nt == 1 && !wide ? 3 : 2; }  // CTAs on an SM: what their registers allow (168, or 255)
 
-template <int NT, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32, attn_ctas(NT, WIDE)) attn_decode_kernel(const AttnArgs a)
+template <int NT, int TERMS_Q, int TERMS_P>
+__global__ void __launch_bounds__(kWarps * 32, attn_ctas(NT, TERMS_Q == 2)) attn_decode_kernel(const AttnArgs a)
 {
     extern __shared__ __align__(128) uint8_t raw_smem[];
     AttnSmem &sm = *reinterpret_cast<AttnSmem *>(raw_smem);
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kWarps * 32, attn_ctas(NT, WIDE)) attn_decode_
         const int len = a.seq_len[w.seq];
         const int kvh = w.sub / a.blocks, hb = w.sub - kvh * a.blocks;
         const int h0 = kvh * a.group + hb * 8 * NT, nh = min(8 * NT, a.group - hb * 8 * NT);
-        Segment<NT, WIDE> sg;
+        Segment<NT, TERMS_Q> sg;
         begin_segment(a, sg, w.seq, h0, nh);
         for (int u = u0; u < u1; ++u) {
             const int k = taken % kStagesW;
@@ -724,9 +724,9 @@ __global__ void __launch_bounds__(kWarps * 32, attn_ctas(NT, WIDE)) attn_decode_
             if (!(absent >> k & 1)) {
                 const uint8_t *page = sm.stage[warp][k];
                 if (s.shift == 2) {
-                    if (u * 16 < len) take_unit<NT, WIDE, 1>(sg, page, len - (u >> 1) * kHalf, u & 1);
+                    if (u * 16 < len) take_unit<NT, TERMS_Q, TERMS_P, 1>(sg, page, len - (u >> 1) * kHalf, u & 1);
                 } else if (u * kPage < len) {
-                    take_unit<NT, WIDE, 4>(sg, page, len - u * kPage, 0);
+                    take_unit<NT, TERMS_Q, TERMS_P, 4>(sg, page, len - u * kPage, 0);
                 }
             }
             __syncwarp();
@@ -824,13 +824,13 @@ int attn_nt(int group, bool wide) { return group > 8 && !wide ? 2 : 1; }
 // Warps of one attn_decode launch: all that the SMs hold.
 int attn_warps(const stq_cache *c, int nt, bool wide) { return c->sms * kWarps * attn_ctas(nt, wide); }
 
-template <int NT, bool WIDE>
+template <int NT, int TERMS_Q, int TERMS_P>
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t s)
 {
     const int smem = static_cast<int>(sizeof(AttnSmem));
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<NT, TERMS_Q, TERMS_P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    attn_decode_kernel<NT, WIDE><<<a.warps / kWarps, kWarps * 32, smem, s>>>(a);
+    attn_decode_kernel<NT, TERMS_Q, TERMS_P><<<a.warps / kWarps, kWarps * 32, smem, s>>>(a);
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -1009,7 +1009,9 @@ stq_status stq_attn_decode(stq_cache *c, const int32_t *page_table, int32_t max_
     a.part = static_cast<float *>(workspace);
     a.waits = stq::waits();
     a.warps = stq::attn_warps(c, nt, wide);
-    const auto launch = wide ? stq::launch_attn<1, true> : nt == 2 ? stq::launch_attn<2, false> : stq::launch_attn<1, false>;
+    const auto launch = wide                 ? stq::launch_attn<1, 2, 2>
+                        : dtype == STQ_F16 ? (nt == 2 ? stq::launch_attn<2, 1, 2> : stq::launch_attn<1, 1, 2>)
+                                           : (nt == 2 ? stq::launch_attn<2, 1, 1> : stq::launch_attn<1, 1, 1>);
     const cudaError_t e = launch(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STQ_OK : stq::cuda_fail(e, "attention launch");
 }

@@ -95,6 +95,40 @@ def test_fp32_rows_over_many_shares(lens):
     s.check_fp32(s.attend())
 
 
+class _Fp16(_Sequences):
+    def check_fp16(self, y):
+        """As fp32 rows, but for y, which is rounded once (half a step, and half of the smallest)."""
+        got = y.float().cpu().numpy().astype(np.float64)
+        k, v = (_quantized(x.float().cpu().numpy()).astype(np.float64) for x in (self.k, self.v))
+        q = self.q.float().cpu().numpy().astype(np.float64)
+        g, at = self.heads // self.kv_heads, 0
+        for i, m in enumerate(self.lens):
+            for h in range(self.heads):
+                kk, vv = k[at:at + m, h // g], v[at:at + m, h // g]
+                x = kk @ q[i, h] * 128 ** -0.5
+                p = np.exp(x - x.max())
+                p /= p.sum()
+                ref = p @ vv
+                delta = (np.abs(kk) @ np.abs(q[i, h])).max() * 128 ** -0.5 * 2.0 ** -19
+                s_max = np.abs(vv).max() / 7 * 1.01
+                small = 2.0 ** -36 * p.max() * max(1.0, 2 * s_max) * (1 + s_max) * 7 * m
+                tol = small + (2.0 ** -18 + 2 * delta + 2.0 ** -20) * (p @ np.abs(vv)) + 1.001 * 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+                bad = ~(np.abs(got[i, h] - ref) <= tol)
+                assert not bad.any(), (i, h, m, np.abs(got[i, h] - ref)[bad][:4], tol[bad][:4])
+            at += m
+
+
+@pytest.mark.parametrize("heads, kv_heads", [(1, 1), (8, 2), (9, 1), (32, 2), (40, 2)])
+@pytest.mark.parametrize("lens", [[1, 63, 64, 65, 200, 1000], [9], [20000]])
+def test_fp16_rows_are_rounded_once(heads, kv_heads, lens):
+    """No error beside the output's own rounding, which one binary16 value for a weight would double."""
+    s = _Fp16(lens, heads, kv_heads, "fp16", seed=36)
+    s.append()
+    y = s.attend()
+    s.check_fp16(y)
+    assert torch.equal(y, s.attend())
+
+
 @pytest.mark.parametrize("pages", [2 ** 25, 2 ** 31 - 1, -1])
 def test_tables_too_wide_for_a_length_are_refused(pages):
     """Lengths up to 64 max_pages are counted in 31 bits."""
