@@ -425,6 +425,9 @@ typedef struct {
  *              aligned, owned by the caller; its content need not be kept between
  *              calls.  Calls that may overlap on the GPU need one each, and a
  *              state each.  fp32 rows need none (NULL and 0 will do).
+ * Long prompts of 16-bit rows go in chunks of 64 tokens.  In y the factors of every
+ * product are then rounded to 11 bits (bf16), or those of q with the state at the
+ * chunk's start alone (fp16), beside y's own rounding.
  * A NaN in a token's q makes its y of that head NaN; one in its k, v, beta or alpha
  * (or in the starting state) the state and y that depend on it, from that token on,
  * and with 16-bit rows y of up to 63 tokens before it may be NaN too.  A state that

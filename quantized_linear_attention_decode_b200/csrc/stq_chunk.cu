@@ -13,12 +13,16 @@
 // Precision.  The state has to come out as the recurrence in fp32 gives it.  k is a
 // 16-bit value, exact in tf32 (11 bits); X_0, V - K X_0, T and D U are fp32 values
 // and enter the tensor core as two tf32 terms, x = hi + lo, 2^-21 of x left: 2 products
-// against k, 3 of the 4 for T times a vector.  Y is rounded to 16 bits: of R Q, P and U one
-// term each, rounded to nearest (2^-11).  Sums are fp32.
+// against k, 3 of the 4 for T times a vector.  Y is rounded to 16 bits: in bf16 one term each
+// of R Q, X_0, P and U, rounded to nearest (2^-11), is below that.  In fp16 it would make the
+// error 1.8 times that of the output's own rounding, nearly all of it by P and U, which enter as
+// two terms (670 us in place of 624 on two prompts of 8192 tokens; what is left is 1.1 times).
+// Sums are fp32.
 //
 // What is no number stays none.  A NaN in q is one in its row of P; one in X_0, v or the decays is one in a whole column of
 // V - diag(R) K X_0 (products with zeros keep it), so of U, Y and X_C; one in k or b in rows of T, so in U.  So P and U
-// alone take care to keep it.  Y has it from the chunk's first token on, since P's zeros above the diagonal meet U's rows.
+// alone take care to keep it (where they are two terms, the second does).  Y has it from the chunk's first token on, since P's
+// zeros above the diagonal meet U's rows.
 #include <cmath>
 
 #include "stq_host.h"
@@ -62,6 +66,10 @@ __device__ __forceinline__ float tf32_hi_or_nan(float x) { return isnan(x) ? x :
 
 // The same by cutting, for a first term whose rest follows: what the tensor core cuts off the rest is 2^-21 of x.
 __device__ __forceinline__ float tf32_cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+
+// Whether P and U enter Y as two terms.
+template <bool BF16>
+constexpr bool kTwoTerms = !BF16;
 
 // Two neighbouring registers of a row as a pair, for packed arithmetic.
 __device__ __forceinline__ float2 pair_at(const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); }
@@ -336,7 +344,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
             }
             const float beta = s.beta[t];
             const float2 a = make_float2(i < t ? beta * (r.x * kk[nt][2 * half]) : 0.0f, i + 1 < t ? beta * (r.y * kk[nt][2 * half + 1]) : 0.0f);
-            const float2 p = make_float2(i <= t ? tf32_hi_or_nan(r.x * qk[nt][2 * half]) : 0.0f, i + 1 <= t ? tf32_hi_or_nan(r.y * qk[nt][2 * half + 1]) : 0.0f);
+            float2 p = make_float2(i <= t ? r.x * qk[nt][2 * half] : 0.0f, i + 1 <= t ? r.y * qk[nt][2 * half + 1] : 0.0f);
+            if (!kTwoTerms<BF16>) p = make_float2(tf32_hi_or_nan(p.x), tf32_hi_or_nan(p.y));
             *reinterpret_cast<float2 *>(&s.m.a[t][i]) = a;
             *reinterpret_cast<float2 *>(out->p + block_of(warp, nt / 2) + (t & 15) * 16 + (i & 15)) = p;
         }
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
 // warps that run ahead.  Columns of tensor memory:
 //     0  X^T, the sum that the chunk's update goes onto, scaled by R_63 beforehand
 //   128  X_0^T hi; then (T (V - R K X_0))^T in two parts; then (D U)^T hi | lo
-//   256  X_0^T lo; then (V - R K X_0)^T hi | lo
+//   256  X_0^T lo; then (V - R K X_0)^T hi | lo; then U^T lo where it is needed
 //   384  (K X_0)^T; then U^T hi
 //   448  (diag(R) Q X_0)^T, then Y^T
 // A product of 8 deep takes about 64 cycles at 128 columns and 45 at 64, for its A operand's
@@ -396,8 +405,22 @@ constexpr int kChunkThreads = 512;  // four warpgroups; warp 15 only hands its r
 // (2 * 152 + 128 + 80 = 4 * 128); where a branch spills instead, the walk takes up to twice as long
 constexpr int kGroupRegs = 152, kOtherRegs = 80;
 constexpr uint32_t kColX = 0, kColHi = 128, kColLo = 256, kColK = 384, kColY = 448;
+// U's second term, of tokens 32 half .. + 31: the parts of X_0^T lo that are written last
+constexpr __device__ uint32_t rest_column(int half) { return kColLo + 64 * half + 32; }
 
-struct __align__(1024) ChunkSmem {
+// P's second term, on and below the diagonal: 64 rows of the first 32 tokens, the last 32 rows of the others.
+constexpr int kRestBlock = kC * 128, kRestBytes = kRestBlock + kC / 2 * 128;
+template <bool TWO_TERMS>
+struct __align__(1024) Rest {
+    uint8_t p_rest[kRestBytes];
+};
+template <>
+struct __align__(1024) Rest<false> {
+    static constexpr uint8_t *p_rest = nullptr;
+};
+
+template <bool BF16>
+struct __align__(1024) ChunkSmem : Rest<kTwoTerms<BF16>> {
     uint8_t kq[2 * kC * kD * 4];  // 4 blocks of 32 dims: 128 rows of 128 bytes, K's and Q's
     uint8_t kt[kC * kD * 4];      // 2 blocks of 32 tokens: 128 rows
     uint8_t t[2 * kC * kC * 4];   // 2 blocks of 32 tokens: 128 rows, T's hi and lo
@@ -407,12 +430,13 @@ struct __align__(1024) ChunkSmem {
     struct {
         float r[kC], d[kC];
     } rd[2];
-    unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, tp_full, tp_empty, v_full, v_empty;
+    unsigned long long kq_raw, kq_full, kq_empty, kt_full, kt_empty, tp_raw_full, t_full, t_empty, p_full, p_empty, v_full, v_empty;
     unsigned long long x_full[2], k_done, r_full, u_done, u_full, y_done, x_done, drained;
     unsigned long long before;  // chunks of the entries before this one
     uint32_t tmem;
     int item;
 };
+static_assert(sizeof(ChunkSmem<false>) + 1024 <= 232448, "shared memory of a CTA");
 
 __device__ __forceinline__ void tc_mma_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
@@ -459,7 +483,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                                                               const __grid_constant__ CUtensorMap v_map, PoolView pool, PromptIO io)
 {
     extern __shared__ uint8_t raw_smem[];
-    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    ChunkSmem<BF16> &sm = *reinterpret_cast<ChunkSmem<BF16> *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, tid = threadIdx.x;
     const int H = pool.H, h = blockIdx.x % H;
     // long prompts first: the entry of this rank by length (all CTAs agree on the order); in their order where
@@ -514,8 +538,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             init(sm.kq_empty, 1);
             init(sm.kt_full, kFeedThreads);
             init(sm.kt_empty, 1);
-            init(sm.tp_full, kSideThreads);
-            init(sm.tp_empty, 1);
+            init(sm.t_full, kSideThreads);
+            init(sm.t_empty, 1);
+            init(sm.p_full, kSideThreads);
+            init(sm.p_empty, 1);
             init(sm.kq_raw, 1);
             init(sm.tp_raw_full, 1);
             init(sm.v_full, 1);
@@ -629,6 +655,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                 reinterpret_cast<uint4 *>(sm.t)[i] = make_uint4(0, 0, 0, 0);
                 reinterpret_cast<uint4 *>(sm.t)[i + kC * kC / 4] = make_uint4(0, 0, 0, 0);
                 reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0, 0, 0, 0);
+                if (kTwoTerms<BF16> && i < kRestBytes / 16) reinterpret_cast<uint4 *>(sm.p_rest)[i] = make_uint4(0, 0, 0, 0);
             }
             const auto fetch_tp = [&](int c) {
                 const uint32_t bar = smem_addr(&sm.tp_raw_full);
@@ -647,24 +674,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             }
             all_agree<1, kSideThreads>(true);
             for (int c = 0; c < chunks; ++c) {
-                // (ok may be false in the thread that fetches: the others learn it below)
-                ok = ok && wait(sm.tp_raw_full, c & 1) && (c == 0 || wait(sm.tp_empty, (c & 1) ^ 1));
-                // ten blocks each of T and P, ten vectors a thread
-#pragma unroll
-                for (int i = 0; i < 10 && ok; ++i) {
+                // ten blocks each of T and P, ten vectors a thread; T's place is free before P's
+                const auto place = [&](int i, int *row, int *col) {
                     const int x = ft + kSideThreads * i, blk = x / (kBlockFloats / 4), in = x % (kBlockFloats / 4) * 4;
                     const int bi = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, bj = blk - bi * (bi + 1) / 2;
-                    const int row = 16 * bi + in / 16, col = 16 * bj + in % 16;
-                    const uint32_t at = swizzled(2 * kC, row, col);
-                    const float4 tv = *reinterpret_cast<const float4 *>(sm.tp_raw + 4 * x);
+                    *row = 16 * bi + in / 16;
+                    *col = 16 * bj + in % 16;
+                    return 4 * x;
+                };
+                // (ok may be false in the thread that fetches: the others learn it below)
+                ok = ok && wait(sm.tp_raw_full, c & 1) && (c == 0 || wait(sm.t_empty, (c & 1) ^ 1));
+#pragma unroll
+                for (int i = 0; i < 10 && ok; ++i) {
+                    int row, col;
+                    const float4 tv = *reinterpret_cast<const float4 *>(sm.tp_raw + place(i, &row, &col));
                     const float4 hi = make_float4(tf32_hi(tv.x), tf32_hi(tv.y), tf32_hi(tv.z), tf32_hi(tv.w));
+                    const uint32_t at = swizzled(2 * kC, row, col);
                     *reinterpret_cast<float4 *>(sm.t + at) = hi;
                     *reinterpret_cast<float4 *>(sm.t + kC * 128 + at) = make_float4(tv.x - hi.x, tv.y - hi.y, tv.z - hi.z, tv.w - hi.w);
-                    *reinterpret_cast<float4 *>(sm.p + swizzled(kC, row, col)) = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + 4 * x);
                 }
                 if (ok) {
                     fence_async_smem();
-                    barrier_arrive(smem_addr(&sm.tp_full));
+                    barrier_arrive(smem_addr(&sm.t_full));
+                    ok = c == 0 || wait(sm.p_empty, (c & 1) ^ 1);
+                }
+#pragma unroll (kTwoTerms<BF16> ? 5 : 10)  // (all ten spill there, which costs the walk 8 %)
+                for (int i = 0; i < 10 && ok; ++i) {
+                    int row, col;
+                    float4 pv = *reinterpret_cast<const float4 *>(sm.tp_raw + kTriangle + place(i, &row, &col));
+                    if (kTwoTerms<BF16>) {
+                        const float4 first = make_float4(tf32_hi(pv.x), tf32_hi(pv.y), tf32_hi(pv.z), tf32_hi(pv.w));
+                        // (rows below 32 have no columns from 32 on; a row's place in its group of eight is the same in both)
+                        const uint32_t to = col < 32 ? swizzled(kC, row, col) : kRestBlock + swizzled(kC / 2, row - 32, col - 32);
+                        *reinterpret_cast<float4 *>(sm.p_rest + to) = make_float4(pv.x - first.x, pv.y - first.y, pv.z - first.z, pv.w - first.w);
+                        pv = first;
+                    }
+                    *reinterpret_cast<float4 *>(sm.p + swizzled(kC, row, col)) = pv;
+                }
+                if (ok) {
+                    fence_async_smem();
+                    barrier_arrive(smem_addr(&sm.p_full));
                 }
                 ok = all_agree<1, kSideThreads>(ok);  // all have read what comes next over it
                 if (!ok) break;
@@ -677,7 +726,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             if (ok && ft == 0) wait(sm.v_full, (chunks - 1) & 1);  // lands, whatever became of those who wanted it
         } else if (warp == 12) {
             // ------------------------------------------------ products
-            constexpr uint32_t n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
+            constexpr uint32_t n32 = tc_idesc(2, 128, 32, false), n64 = tc_idesc(2, 128, 64, false), n128 = tc_idesc(2, 128, 128, false);
             const uint32_t kq = smem_addr(sm.kq), kt = smem_addr(sm.kt), tt = smem_addr(sm.t), p = smem_addr(sm.p);
             // step s of 8 in an operand of blocks of 32 columns and `rows` rows
             const auto step = [](uint32_t base, int rows, int s) { return tc_desc(base + (s >> 2) * rows * 128 + (s & 3) * 32, 16, 1024); };
@@ -709,7 +758,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     }
                     __syncwarp();
                 }
-                ok = ok && wait(sm.tp_full, phase) && wait(sm.r_full, phase);
+                ok = ok && wait(sm.t_full, phase) && wait(sm.r_full, phase);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -717,6 +766,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll
                     for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColHi, tmem + kColLo + 64 + 8 * s, step(tt, 128, s), n64, true);
                     tc_commit(smem_addr(&sm.u_done));
+                    tc_commit(smem_addr(&sm.t_empty));
                 }
                 __syncwarp();
                 ok = ok && wait(sm.kt_full, phase) && wait(sm.u_full, phase);
@@ -726,10 +776,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
                     for (int s = 0; s < 16; ++s) tc_mma_tf32(tmem + kColX, tmem + kColHi + 8 * s, step(kt, 128, s & 7), n128, true);
                     tc_commit(smem_addr(&sm.x_done));
                     tc_commit(smem_addr(&sm.kt_empty));
+                }
+                __syncwarp();
+                ok = ok && wait(sm.p_full, phase);
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s) tc_mma_tf32(tmem + kColY, tmem + kColK + 8 * s, step(p, 64, s), n64, true);
+                    if (kTwoTerms<BF16>) {
+                        const uint32_t rest = smem_addr(sm.p_rest);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tc_mma_tf32(tmem + kColY, tmem + rest_column(0) + 8 * s, step(p, 64, s), n64, true);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tc_mma_tf32(tmem + kColY + 32, tmem + rest_column(1) + 8 * s, step(p + kC * 128 + 32 * 128, 64, s), n32, true);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tc_mma_tf32(tmem + kColY, tmem + kColK + 8 * s, step(rest, 64, s), n64, true);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tc_mma_tf32(tmem + kColY + 32, tmem + kColK + 32 + 8 * s, step(rest + kRestBlock, 32, s), n32, true);
+                    }
                     tc_commit(smem_addr(&sm.y_done));
-                    tc_commit(smem_addr(&sm.tp_empty));
+                    tc_commit(smem_addr(&sm.p_empty));
                 }
                 ok = __all_sync(0xffffffffu, ok);
             }
@@ -845,12 +911,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             for (int i = 0; i < 32; i += 2) put_pair(x + i, __fadd2_rn(pair_at(x + i), pair_at(w + i)));
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(tf32_hi(__uint_as_float(x[i])));
-            // One NaN in a column of U makes its whole column of Y one, as it should be (below): zero times U is added to an element.
-            float2 none[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            if (!kTwoTerms<BF16>) {
+                // One NaN in a column of U makes its whole column of Y one, as it should be (top of the file): zero times U is added to an element.
+                float2 none[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) none[i >> 1 & 1] = __ffma2_rn(pair_at(x + i), make_float2(0.0f, 0.0f), none[i >> 1 & 1]);
-            w[0] = __float_as_uint(__uint_as_float(w[0]) + ((none[0].x + none[0].y) + (none[1].x + none[1].y)));
+                for (int i = 0; i < 32; i += 2) none[i >> 1 & 1] = __ffma2_rn(pair_at(x + i), make_float2(0.0f, 0.0f), none[i >> 1 & 1]);
+                w[0] = __float_as_uint(__uint_as_float(w[0]) + ((none[0].x + none[0].y) + (none[1].x + none[1].y)));
+            }
             tmem_store32(base + kColK + 32 * half, w);
+            if (kTwoTerms<BF16>) {  // where the next chunk's X_0 has not come yet
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) put_pair(w + i, minus(pair_at(x + i), pair_at(w + i)));
+                tmem_store32(base + rest_column(half), w);
+            }
 #pragma unroll
             for (int i = 0; i < 32; i += 2) put_pair(x + i, __fmul2_rn(pair_at(x + i), *reinterpret_cast<const float2 *>(&rd.d[32 * half + i])));
 #pragma unroll
@@ -924,7 +997,7 @@ cudaError_t launch(const PoolView &p, const PromptIO &io, cudaStream_t stream)
     if (!make_map(&q, io.q, io.dtype, io.span.total, p.H, 1, kC) || !make_map(&k, io.k, io.dtype, io.span.total, p.H, 1, kC) ||
         !make_map(&v, io.v, io.dtype, io.span.total, p.H, 1, kC))
         return cudaErrorInvalidValue;
-    const int prep = static_cast<int>(sizeof(PrepSmem)), smem = static_cast<int>(sizeof(ChunkSmem)) + 1024;
+    const int prep = static_cast<int>(sizeof(PrepSmem)), smem = static_cast<int>(sizeof(ChunkSmem<BF16>)) + 1024;
     cudaError_t e = cudaFuncSetAttribute(prepare_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from quantized_linear_attention_decode_b200 import stq
-from test_gpu_prompt import _Prompts, _cuda
+from test_gpu_prompt import _Prompts, _cuda, _f64, recurrence
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -145,3 +145,19 @@ def test_entries_of_few_tokens_each(kind, lens, launches):
     assert stq.stq_launch_count() - before == launches
     stq.stq_pool_check(s.pool)
     s.check()
+
+
+@pytest.mark.parametrize("lens", [[64, 64, 33, 1, 50], [64] * 12])
+@pytest.mark.parametrize("heads", [2, 16])
+def test_fp16_rows_are_rounded_once(heads, lens):
+    """Prompts of one chunk from the zero state: y = P U, P and U two terms each (2^-20 of every product is left, and the
+    recurrence's 1e-5), is off by half a step of itself; one term each would add two more roundings of that size."""
+    s = _Prompts(lens, heads, "fp16", seed=60, state=False)
+    s.run()
+    y = _f64(s.y)
+    for e, m in enumerate(s.lens):
+        a, b = s.starts[e], s.starts[e + 1]
+        want, _, size = recurrence(*(_f64(t[a:b]) for t in (s.q, s.k, s.v, s.beta, s.alpha)), s.S0[e])
+        tol = 1e-5 * np.abs(want).max((0, 2), keepdims=True) + 1.001 * 2.0 ** -11 * np.abs(want) + 2.0 ** -19 * size + 2.0 ** -25
+        bad = ~(np.abs(y[a:b] - want) <= tol)
+        assert not bad.any(), (e, m, np.abs(y[a:b] - want)[bad][:4], tol[bad][:4])
