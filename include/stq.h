@@ -450,10 +450,11 @@ stq_status stq_prompt_step(stq_pool *pool, const int32_t *req_idx, const int32_t
  * keys up to j + Lk - Lq (a piece of a prompt behind earlier keys; all of them
  * new when Lq = Lk):
  *   y[j][h] = sum_t softmax_t(scale q[j][h] . k[t][g]) v[t][g],  g = h / (num_heads / num_kv_heads).
- * A query that sees no key (Lq > Lk) has y = 0.
+ * A query that sees no key (Lq > Lk) has y = 0.  n == 0 or total_q == 0 is a no-op.
  *   q_start, k_start: device int32 [n + 1].  A range that is not within
  *             [0, total_q] or [0, total_k], or runs backwards, is skipped (its y left
- *             as it was) and reported.
+ *             as it was) and reported.  Query ranges that overlap have undefined
+ *             results; key ranges may.
  *   q, k, v:  device rows of `dtype` (STQ_BF16 or STQ_F16; STQ_F32 returns
  *             STQ_ERR_UNSUPPORTED), total_q tokens of num_heads heads and total_k of
  *             num_kv_heads; positive strides (else STQ_ERR_UNSUPPORTED).

@@ -22,9 +22,9 @@
 // so that the next loads and scores stand behind this item's last weights and its output.
 // Blocks are ordered by tokens from a sequence's end, then heads: the longest first.
 // A key tile of which 64 keys are seen at most is half a tile for all three.
-// 24 prompts to 2000 tokens: 319 us with a CTA an item, 283 with the heads outermost
-// (8192 tokens 534), 274 so; 582 for the 8192 tokens where a CTA asked as soon as it began
-// an item, and kept the next one waiting.
+// When this was chosen, 24 prompts to 2000 tokens took 319 us with a CTA an item, 283 with the
+// heads outermost (8192 tokens 534), 274 so (520); 582 for the 8192 tokens where a CTA asked as
+// soon as it began an item, and kept the next one waiting.
 //
 // The running maximum that P is taken against moves only when a score lies more than
 // 2^8 above it (P then stays below 2^8, within fp16's range), so O is rescaled in
@@ -39,8 +39,8 @@
 // behind the other tile.  So taking a part of the exponentials on the fp32 pipe instead
 // (a polynomial for 1, 2 or 3 of 8) cost 1, 3 and 7 %, and two warps that issue one
 // tile's products each, interleaved in the tensor core, 4 %.
-// 32 query and 8 key heads, bf16: 8192 tokens 520 us, 1057 TFLOP/s; 24 prompts to 2000
-// tokens 274 us, 740 TFLOP/s of visible pairs.
+// 32 query and 8 key heads, bf16: 8192 tokens 536 us, 1025 TFLOP/s; 24 prompts to 2000
+// tokens 278 us, 730 TFLOP/s of visible pairs.
 #include <algorithm>
 #include <cmath>
 

@@ -229,8 +229,8 @@ __device__ __forceinline__ void below(PrepSmem &s)
 // shared-memory accesses.  The inverse: its diagonal blocks of 16 by substitution, a thread a
 // column, the others by block products in three tf32 terms (in fp32 on the other pipe they
 // took four times the accesses).  R_ti is put together from products within groups of eight
-// tokens and of whole groups between them.  8832 chunks and heads: 137 us, 42 % of the issue
-// slots, 37 % of DRAM.
+// tokens and of whole groups between them.  8832 chunks and heads: 143 us, 42 % of the issue
+// slots, 35 % of DRAM.
 template <bool BF16>
 __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, int H)
 {
@@ -394,8 +394,9 @@ __global__ void __launch_bounds__(kPrepThreads, 5) prepare_kernel(PromptIO io, i
 //   448  (diag(R) Q X_0)^T, then Y^T
 // A product of 8 deep takes about 64 cycles at 128 columns and 45 at 64, for its A operand's
 // sake, so K and Q stand under each other for the hi term, and T's two terms for R's.
-// Bound by the chain of all but Y's with what stands between them: 3.7 us a chunk, 2 prompts of
-// 8192 tokens with 32 heads 473 us; 24 prompts to 1500 tokens 262 us, tensor pipe 45 % busy.
+// Bound by the chain of all but Y's with what stands between them: 3.8 us a chunk in bf16, 4.2 in
+// fp16 (2 prompts of 8192 tokens with 32 heads 540 us); 24 prompts to 1500 tokens in bf16 285 us,
+// tensor pipe 45 % busy.
 
 constexpr int kGroupThreads = 256;  // warps 0-7: two for each quarter of the lanes, half of the columns each
 constexpr int kFeedThreads = 128;   // warps 8-11; warp 12 issues the products

@@ -60,7 +60,6 @@ struct DeviceGuard {
 // Bytes of one element of a stq_dtype, 0 if it is none.
 inline int dtype_bytes(int32_t dtype) { return dtype == STQ_F32 ? 4 : dtype == STQ_BF16 || dtype == STQ_F16 ? 2 : 0; }
 
-// Every head row of `r` starts on a 16-byte boundary.
 // Launches a kernel whose CTAs may start, and get as far as their wait for the previous grid, while the last CTAs
 // of the stream's previous kernel run.  Such a kernel waits in every CTA, so that its end is the end of both.
 template <typename... Args>
@@ -81,6 +80,7 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int s
     return e;
 }
 
+// Every head row of `r` starts on a 16-byte boundary.
 inline bool rows_aligned(const stq_rows *r, int32_t dtype)
 {
     const int64_t per = 16 / dtype_bytes(dtype);
