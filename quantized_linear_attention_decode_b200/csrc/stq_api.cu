@@ -187,7 +187,9 @@ stq::PoolView view(stq_pool *p)
     v.n_pivot_heads = p->n_pivot_heads;
     v.t = p->t;
     v.err = p->d_err;
-    static_cast<stq::Waits &>(v) = stq::waits();
+    const stq::Waits w = stq::waits();
+    v.wait_ns = w.wait_ns;
+    v.stall_tx = w.stall_tx;
     return v;
 }
 

@@ -52,7 +52,7 @@ struct Waits {
     uint32_t stall_tx;
 };
 
-struct PoolView : Waits {
+struct PoolView {
     uint8_t *pages;      // [R][S][slot_bytes]
     size_t slot_bytes;
     int R, S, H;
@@ -66,6 +66,8 @@ struct PoolView : Waits {
     int n_pivot_heads;   // GDN: heads held in FP16 (their own kernel), listed in t.pivot_head
     Tables t;
     uint32_t *err;
+    unsigned long long wait_ns;  // as in Waits
+    uint32_t stall_tx;
 };
 
 struct DecodeIO {
